@@ -24,7 +24,9 @@ OP = {"fwd": 0, "bwd_w": 1, "bwd_h": 2, "fwd_bce": 3, "step": 4, "fixed_fwd": 5,
 DH_MODE = {"atomic": 0, "det": 1, "deterministic": 1, 0: 0, 1: 1}
 
 # name -> (restype, argtypes); P = pointer, I = int64, S = size_t, F = float, M = int
+# D = double, U = uint64
 _P, _I, _S, _F, _M = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+_D, _U = ctypes.c_double, ctypes.c_uint64
 SIGNATURES = {
     "haste_workspace_size": (_S, [_M, _I, _I, _I, _I, _I, _M]),
     "haste_fwd": (_M, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _S, _P]),
@@ -67,6 +69,16 @@ SIGNATURES = {
     "haste_validate_idx": (_M, [_P, _I, _I, _I, _P, _P]),
     "haste_validate_labels": (_M, [_P, _P, _I, _I, _P, _P]),
     "haste_workspace_status": (_M, [_P, _P, _P]),
+    "haste_dropout": (_M, [_P, _P, _P, _I, _I, _I, _I, _D, _U, _U, _P, _M, _P]),
+    "haste_add_norm": (_M, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _D, _U, _U, _P, _M, _P]),
+    "haste_add_norm_workspace_size": (_S, [_I, _I]),
+    "haste_add_norm_bwd": (_M, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _D, _U, _U, _P, _M, _P, _S, _P]),
+    "haste_quantize_rows": (_M, [_P, _P, _P, _I, _I, _I, _M, _P]),
+    "haste_score_a8w8": (_M, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "haste_softmax_workspace_size": (_S, [_I, _I, _I, _M]),
+    "haste_softmax_workspace_min": (_S, [_I, _I, _I, _M]),
+    "haste_softmax_loss": (_M, [_P, _P, _P, _P, _F, _P, _P, _P, _I, _I, _I, _I, _I, _M, _P, _S, _P]),
+    "haste_softmax_step": (_M, [_P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _M, _P, _S, _P]),
     "haste_test_set_turn_spins": (None, [_M]),
     "haste_status_string": (ctypes.c_char_p, [_M]),
     "haste_version": (ctypes.c_char_p, []),
@@ -630,6 +642,247 @@ def order_slots(idx, W=None, G=None, perm=False, stream=None):
     p = torch.empty(K, F, dtype=torch.uint8, device=idx.device) if perm else None
     _check("haste_order_slots", lib().haste_order_slots(_ptr(idx), _ptr(W), _ptr(p), K, Gv, F, _stream(idx, stream)))
     return p
+
+
+# ------------------------------------------------ norm, dropout, scoring, softmax loss
+
+_DTYPES = None
+
+
+def _dtype_code(t):
+    """haste_dtype of a tensor (bf16, fp16, fp32)."""
+    global _DTYPES
+    if _DTYPES is None:
+        torch = _torch()
+        _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _ld(t, shape, dtype, what):
+    """Row stride (elements) of a 2-D tensor whose rows are contiguous."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{what} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    ld = t.stride(0)
+    if (t.stride(1) != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+        raise ValueError(f"{what} must have contiguous rows, no two overlapping")
+    return ld if shape[0] > 1 else max(ld, shape[1])
+
+
+def _dense(t, shape, dtype, what):
+    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return t
+
+
+def _codes(t, what):
+    """E4M3 codes: a contiguous float8_e4m3fn (or uint8) matrix."""
+    torch = _torch()
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float8_e4m3fn (or uint8) matrix")
+    return t
+
+
+def _together(x, *others):
+    """Every tensor of a call on one device (a host pointer in a kernel would fault)."""
+    d = x.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError(f"all tensors of a call must be on one device, got {d} and {t.device}")
+
+
+_MASK64 = (1 << 64) - 1
+
+
+def dropout(x, p, seed, offset=0, residual=None, out=None, offset_dev=None, stream=None):
+    """y = residual + dropout(x), the mask drawn from (seed, offset) and the position alone; the
+    gradient of x is dropout(dy, p, seed, offset).  offset_dev: int64 tensor of one element added to
+    offset when the call runs (for captured graphs)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be rows x cols")
+    code, (rows, cols) = _dtype_code(x), x.shape
+    ldx = _ld(x, x.shape, x.dtype, "x")
+    ldr = _ld(residual, x.shape, x.dtype, "residual") if residual is not None else 0
+    if out is None:
+        out = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
+    else:
+        _dense(out, x.shape, x.dtype, "out")
+    _together(x, residual, out, offset_dev)
+    _check("haste_dropout", lib().haste_dropout(
+        _ptr(x), _ptr(residual), _ptr(out), rows, cols, ldx, ldr, float(p), seed & _MASK64, offset & _MASK64,
+        _ptr(offset_dev), code, _stream(x, stream)))
+    return out
+
+
+def add_norm(x, gamma, residual=None, eps=1e-6, p=0.0, seed=0, offset=0, want_y=True, want_a8=False, out=None,
+             offset_dev=None, stream=None):
+    """v = residual + dropout(x); y = v / sqrt(mean v^2 + eps) gamma per row.  Returns dict(sum = v, and
+    y and rstd with want_y, and q (E4M3) and scale (one per row) with want_a8)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be rows x cols")
+    code, (rows, cols) = _dtype_code(x), x.shape
+    ldx = _ld(x, x.shape, x.dtype, "x")
+    ldr = _ld(residual, x.shape, x.dtype, "residual") if residual is not None else 0
+    _dense(gamma, (cols,), x.dtype, "gamma")
+    if out is None:
+        out = {"sum": torch.empty(rows, cols, dtype=x.dtype, device=x.device)}
+        if want_y:
+            out["y"] = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
+            out["rstd"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if want_a8:
+            out["q"] = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
+            out["scale"] = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        for k in ("sum", "y"):
+            _dense(out.get(k), x.shape, x.dtype, k)
+        for k in ("rstd", "scale"):
+            _dense(out.get(k), (rows,), torch.float32, k)
+        if out.get("q") is not None and _codes(out["q"], "q").shape != x.shape:
+            raise ValueError("q must have x's shape")
+    _together(x, gamma, residual, offset_dev, *out.values())
+    _check("haste_add_norm", lib().haste_add_norm(
+        _ptr(x), _ptr(residual), _ptr(gamma), _ptr(out.get("sum")), _ptr(out.get("y")), _ptr(out.get("q")),
+        _ptr(out.get("scale")), _ptr(out.get("rstd")), rows, cols, ldx, ldr, float(eps), float(p), seed & _MASK64,
+        offset & _MASK64, _ptr(offset_dev), code, _stream(x, stream)))
+    return out
+
+
+def add_norm_workspace_size(rows, cols) -> int:
+    return int(lib().haste_add_norm_workspace_size(rows, cols))
+
+
+def add_norm_bwd(dy, sum, gamma, rstd, dsum=None, p=0.0, seed=0, offset=0, out=None, workspace=None,
+                 offset_dev=None, stream=None):
+    """Backward of add_norm from dy and the forward's sum and rstd; dsum: the gradient reaching `sum` from
+    later layers.  Returns dict(dres, dgamma, and dx when p > 0; without dropout dx is dres)."""
+    torch = _torch()
+    if dy.dim() != 2:
+        raise ValueError("dy must be rows x cols")
+    code, (rows, cols) = _dtype_code(dy), dy.shape
+    lddy = _ld(dy, dy.shape, dy.dtype, "dy")
+    ldds = _ld(dsum, dy.shape, dy.dtype, "dsum") if dsum is not None else 0
+    _dense(sum, dy.shape, dy.dtype, "sum")
+    _dense(gamma, (cols,), dy.dtype, "gamma")
+    _dense(rstd, (rows,), torch.float32, "rstd")
+    if out is None:
+        out = {"dres": torch.empty(rows, cols, dtype=dy.dtype, device=dy.device),
+               "dgamma": torch.empty(cols, dtype=torch.float32, device=dy.device)}
+        if p > 0:
+            out["dx"] = torch.empty(rows, cols, dtype=dy.dtype, device=dy.device)
+    else:
+        for k in ("dres", "dx"):
+            _dense(out.get(k), dy.shape, dy.dtype, k)
+        _dense(out.get("dgamma"), (cols,), torch.float32, "dgamma")
+    ws = workspace
+    if ws is None and out.get("dgamma") is not None:
+        ws = torch.empty(add_norm_workspace_size(rows, cols), dtype=torch.uint8, device=dy.device)
+    _together(dy, sum, gamma, rstd, dsum, offset_dev, ws, *out.values())
+    _check("haste_add_norm_bwd", lib().haste_add_norm_bwd(
+        _ptr(dy), _ptr(sum), _ptr(gamma), _ptr(rstd), _ptr(dsum), _ptr(out["dres"]), _ptr(out.get("dx")),
+        _ptr(out.get("dgamma")), rows, cols, lddy, ldds, float(p), seed & _MASK64, offset & _MASK64,
+        _ptr(offset_dev), code, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dy, stream)))
+    return out
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """E4M3 codes of x with one scale per row (max |x| / 448).  Returns (q, scale)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be rows x cols")
+    code, (rows, cols) = _dtype_code(x), x.shape
+    ldx = _ld(x, x.shape, x.dtype, "x")
+    if q is None:
+        q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
+    elif _codes(q, "q").shape != x.shape:
+        raise ValueError("q must have x's shape")
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _dense(scale, (rows,), torch.float32, "scale")
+    _together(x, q, scale)
+    _check("haste_quantize_rows", lib().haste_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), rows, cols, ldx, code,
+                                                             _stream(x, stream)))
+    return q, scale
+
+
+def score_a8w8(hq, h_scale, Wq, w_scale, Z=None, stream=None):
+    """Z (B x L fp32) = logits of E4M3 features against E4M3 label weights, one scale per row of each."""
+    torch = _torch()
+    _codes(hq, "hq"), _codes(Wq, "Wq")
+    (B, H), L = hq.shape, Wq.shape[0]
+    if Wq.shape[1] != H:
+        raise ValueError("Wq must be L x H")
+    _dense(h_scale, (B,), torch.float32, "h_scale")
+    _dense(w_scale, (L,), torch.float32, "w_scale")
+    if Z is None:
+        Z = torch.empty(B, L, dtype=torch.float32, device=hq.device)
+    else:
+        _dense(Z, (B, L), torch.float32, "Z")
+    _together(hq, h_scale, Wq, w_scale, Z)
+    _check("haste_score_a8w8", lib().haste_score_a8w8(_ptr(hq), _ptr(h_scale), _ptr(Wq), _ptr(w_scale), _ptr(Z),
+                                                       B, H, L, _stream(hq, stream)))
+    return Z
+
+
+def softmax_workspace_size(B, H, L, grad=True, minimum=False) -> int:
+    """Workspace bytes of softmax_step (grad) or softmax_loss; minimum: the least that is accepted, which
+    takes the label space 256 labels at a time."""
+    fn = lib().haste_softmax_workspace_min if minimum else lib().haste_softmax_workspace_size
+    return int(fn(B, H, L, int(grad)))
+
+
+def _softmax(grad, h, W, y_rowptr, y_col, scale, out, workspace, stream):
+    torch = _torch()
+    if h.dim() != 2 or W.dim() != 2 or W.shape[1] != h.shape[1]:
+        raise ValueError("h must be B x H and W L x H")
+    _i32(y_rowptr), _i32(y_col)
+    code, (B, H), L = _dtype_code(h), h.shape, W.shape[0]
+    if y_rowptr.shape != (B + 1,):
+        raise ValueError("y_rowptr must have B + 1 entries")
+    ldh, ldw = _ld(h, h.shape, h.dtype, "h"), _ld(W, W.shape, h.dtype, "W")
+    if out is None:
+        out = {"row_loss": torch.empty(B, dtype=torch.float32, device=h.device),
+               "lse": torch.empty(B, dtype=torch.float32, device=h.device),
+               "loss": torch.empty(1, dtype=torch.float32, device=h.device)}
+        if grad:
+            out["dW"] = torch.empty(L, H, dtype=h.dtype, device=h.device)
+            out["dh"] = torch.empty(B, H, dtype=h.dtype, device=h.device)
+    else:
+        for k, n in (("row_loss", B), ("lse", B), ("loss", 1)):
+            _dense(out[k], (n,), torch.float32, k)
+        if grad:
+            _dense(out["dW"], W.shape, h.dtype, "dW")
+            _dense(out["dh"], h.shape, h.dtype, "dh")
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(softmax_workspace_size(B, H, L, grad), dtype=torch.uint8, device=h.device)
+    _together(h, W, y_rowptr, y_col, ws, *out.values())
+    # a batch of padding alone has no label ids to point at, and reads none
+    col = y_col if y_col.numel() else y_rowptr
+    head = (_ptr(h), _ptr(W), _ptr(y_rowptr), _ptr(col), float(scale))
+    stat = (_ptr(out["row_loss"]), _ptr(out["lse"]), _ptr(out["loss"]))
+    tail = (B, H, L, ldh, ldw, code, _ptr(ws), ws.numel(), _stream(h, stream))
+    if grad:
+        _check("haste_softmax_step",
+               lib().haste_softmax_step(*head, _ptr(out["dW"]), _ptr(out["dh"]), *stat, *tail))
+    else:
+        _check("haste_softmax_loss", lib().haste_softmax_loss(*head, *stat, *tail))
+    return out
+
+
+def softmax_step(h, W, y_rowptr, y_col, scale, out=None, workspace=None, stream=None):
+    """Softmax cross entropy over the dense label matrix W with its gradient; rows without labels are
+    padding.  Returns dict(dW, dh, row_loss, lse, loss)."""
+    return _softmax(True, h, W, y_rowptr, y_col, scale, out, workspace, stream)
+
+
+def softmax_loss(h, W, y_rowptr, y_col, scale, out=None, workspace=None, stream=None):
+    """The loss of softmax_step alone.  Returns dict(row_loss, lse, loss)."""
+    return _softmax(False, h, W, y_rowptr, y_col, scale, out, workspace, stream)
 
 
 def validate_idx(idx, H, stream=None) -> int:

@@ -1,0 +1,218 @@
+// Element types and the counter-based generator shared by the feature
+// operators (norm, dropout, softmax loss, 8-bit scoring).
+#pragma once
+
+#include <type_traits>
+
+#include "common.hpp"
+#include "haste.h"
+
+namespace haste {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+// Sixteen bytes at any element address: global memory takes unaligned
+// 16-byte accesses on this target as one instruction, so rows that start
+// at odd offsets need no path of their own.
+struct __attribute__((packed, aligned(2))) Any16 {
+    u32x4_t v;
+};
+
+__device__ __forceinline__ u32x4_t ldg16_any(const void* p) { return reinterpret_cast<const Any16*>(p)->v; }
+__device__ __forceinline__ void stg16_any(void* p, u32x4_t v) { reinterpret_cast<Any16*>(p)->v = v; }
+
+// Two fp32 -> packed fp16 pair, round to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)lo, (_Float16)hi});
+}
+
+// DT: a haste_dtype.  Values are held as fp32 in registers and rounded once,
+// to nearest even, when they are stored.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    static_assert(DT == HASTE_BF16 || DT == HASTE_F16, "16-bit types");
+    if constexpr (DT == HASTE_BF16) return pack_bf16(lo, hi);
+    else return pack_f16(lo, hi);
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack2(uint32_t p, float& lo, float& hi)
+{
+    if constexpr (DT == HASTE_BF16) {
+        lo = bf16lo_to_f32(p);
+        hi = bf16hi_to_f32(p);
+    } else {
+        const f16x2_t v = __builtin_bit_cast(f16x2_t, p);
+        lo = (float)v[0];
+        hi = (float)v[1];
+    }
+}
+
+template <int DT>
+constexpr int elem_bytes()
+{
+    return DT == HASTE_F32 ? 4 : 2;
+}
+
+// Eight consecutive elements as they lie in memory.
+template <int DT>
+struct Raw8 {
+    u32x4_t a[DT == HASTE_F32 ? 2 : 1];
+};
+
+// Elements i .. i + 7 of p, of which n (1 <= n) exist; the rest read as 0.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const void* p, int64_t i, int64_t n)
+{
+    Raw8<DT> r;
+    const char* q = reinterpret_cast<const char*>(p) + i * elem_bytes<DT>();
+    if (n >= 8) {
+        r.a[0] = ldg16_any(q);
+        if constexpr (DT == HASTE_F32) r.a[1] = ldg16_any(q + 16);
+    } else if constexpr (DT == HASTE_F32) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.a[e / 4][e % 4] = e < n ? w[e] : 0u;
+    } else {
+        const uint16_t* w = reinterpret_cast<const uint16_t*>(q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = 2 * e < n ? w[2 * e] : 0u, hi = 2 * e + 1 < n ? w[2 * e + 1] : 0u;
+            r.a[0][e] = lo | (hi << 16);
+        }
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8])
+{
+    if constexpr (DT == HASTE_F32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r.a[e / 4][e % 4]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) unpack2<DT>(r.a[0][e], v[2 * e], v[2 * e + 1]);
+    }
+}
+
+// v rounded to the type, into elements i .. i + min(8, n) - 1 of p.
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, const float (&v)[8])
+{
+    char* q = reinterpret_cast<char*>(p) + i * elem_bytes<DT>();
+    if constexpr (DT == HASTE_F32) {
+        u32x4_t a, b;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            a[e] = __float_as_uint(v[e]);
+            b[e] = __float_as_uint(v[4 + e]);
+        }
+        if (n >= 8) {
+            stg16_any(q, a);
+            stg16_any(q + 16, b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) reinterpret_cast<float*>(q)[e] = v[e];
+        }
+    } else {
+        u32x4_t a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = pack2<DT>(v[2 * e], v[2 * e + 1]);
+        if (n >= 8) {
+            stg16_any(q, a);
+        } else {
+            uint16_t* w = reinterpret_cast<uint16_t*>(q);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) w[e] = (uint16_t)(a[e / 2] >> (16 * (e % 2)));
+        }
+    }
+}
+
+// v * inv as E4M3 codes (rounded to nearest even from fp32), into bytes
+// i .. i + min(8, n) - 1 of q.
+__device__ __forceinline__ void store_e4m3(uint8_t* q, int64_t i, int64_t n, const float (&v)[8], float inv)
+{
+    uint32_t w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e] * inv, v[4 * e + 1] * inv, 0, false);
+        c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * e + 2] * inv, v[4 * e + 3] * inv, c, true);
+        w[e] = (uint32_t)c;
+    }
+    if (n >= 8) {
+        struct __attribute__((packed, aligned(1))) Any8 {
+            u32x2_t v;
+        };
+        reinterpret_cast<Any8*>(q + i)->v = u32x2_t{w[0], w[1]};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) q[i + e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+    }
+}
+
+// Philox 4x32 with ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel
+// random numbers: as easy as 1, 2, 3", SC 2011): a bijection of a 128-bit
+// counter under a 64-bit key, so any element's bits follow from its
+// position alone and a mask need never be stored.
+struct Philox {
+    uint32_t k0, k1;     // key: the seed
+    uint32_t c2, c3;     // upper half of the counter: the offset
+};
+
+__device__ __forceinline__ u32x4_t philox(const Philox& g, uint64_t block)
+{
+    uint32_t x0 = (uint32_t)block, x1 = (uint32_t)(block >> 32), x2 = g.c2, x3 = g.c3;
+    uint32_t k0 = g.k0, k1 = g.k1;
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)x0 * 0xD2511F53u, b = (uint64_t)x2 * 0xCD9E8D57u;
+        x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
+        x1 = (uint32_t)b;
+        x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+        x3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return u32x4_t{x0, x1, x2, x3};
+}
+
+// Dropout of a rows x cols array.  The eight elements 8 c .. 8 c + 7 of row r
+// take the eight 16-bit halves (low half first) of the Philox words of
+// counter (r ceil(cols / 8) + c, offset); an element is dropped when its
+// half is below thr = round(65536 p) and else multiplied by
+// 65536 / (65536 - thr), so the expectation is exact for the rounded p.
+// One generator call covers eight elements: with 32 bits per element the
+// rounds' 64-bit products, at a quarter of the vector rate, would bound a
+// 16-bit dropout below the memory rate.
+struct Drop {
+    uint32_t thr;                  // 0: nothing is dropped
+    float factor;
+    uint64_t seed, offset;
+    const uint64_t* offset_dev;    // nullable: its value is added to offset
+};
+
+__device__ __forceinline__ Philox drop_generator(const Drop& d)
+{
+    const uint64_t o = d.offset + (d.offset_dev ? *d.offset_dev : 0);
+    return Philox{(uint32_t)d.seed, (uint32_t)(d.seed >> 32), (uint32_t)o, (uint32_t)(o >> 32)};
+}
+
+// Selects rather than multiplies: a dropped NaN or infinity leaves 0.
+__device__ __forceinline__ void drop8(const Drop& d, const Philox& g, uint64_t block, float (&v)[8])
+{
+    const u32x4_t w = philox(g, block);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = (w[e] & 0xffffu) >= d.thr ? v[2 * e] * d.factor : 0.f;
+        v[2 * e + 1] = (w[e] >> 16) >= d.thr ? v[2 * e + 1] * d.factor : 0.f;
+    }
+}
+
+}  // namespace haste

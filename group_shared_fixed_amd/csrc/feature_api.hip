@@ -1,0 +1,255 @@
+// C ABI of the feature operators (norm, dropout, 8-bit scoring, softmax
+// loss): host-side validation, workspace layout and launches.  Every check
+// runs before the first HIP call.
+#include "haste.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "api_util.hpp"
+#include "elem.hpp"
+#include "kernels.hpp"
+
+using namespace haste;
+
+namespace {
+
+constexpr int64_t kMaxLabels = 2147483647LL - 64;
+constexpr int64_t kMaxRows = 1LL << 40;        // rows x cols stays far below 2^63
+
+inline bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+inline size_t elem_size(int dtype) { return dtype == HASTE_F32 ? 4 : 2; }
+
+// Sizes, strides and type of a row-wise call.
+int check_rows(int64_t rows, int64_t cols, int64_t ld0, int64_t ld1, bool has1, int dtype)
+{
+    if (rows < 1 || cols < 1 || ld0 < cols || (has1 && ld1 < cols)) return HASTE_ERR_DIM;
+    if (dtype != HASTE_BF16 && dtype != HASTE_F16 && dtype != HASTE_F32) return HASTE_ERR_UNSUPPORTED;
+    if (rows > kMaxRows || cols > (1LL << 20) || ld0 > (1LL << 21) || (has1 && ld1 > (1LL << 21)))
+        return HASTE_ERR_UNSUPPORTED;
+    return HASTE_OK;
+}
+
+int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, Drop& d)
+{
+    if (!(p >= 0.0 && p <= 1.0)) return HASTE_ERR_DIM;
+    if (offset_dev && !aligned_to(offset_dev, 8)) return HASTE_ERR_ALIGN;
+    d.thr = (uint32_t)std::nearbyint(p * 65536.0);
+    d.factor = d.thr < 65536 ? (float)(65536.0 / (65536.0 - d.thr)) : 0.f;
+    d.seed = seed;
+    d.offset = offset;
+    d.offset_dev = offset_dev;
+    return HASTE_OK;
+}
+
+// Softmax workspace: fixed parts, then the piece of D, whose length follows
+// from the bytes that are left.
+struct SoftmaxLayout {
+    int64_t Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
+    int splits;
+    size_t nv, rows, rank, hit, clse, part, hc, dhp, dz;
+    SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
+    {
+        Bp = round_up(B, kSmRowTile);
+        Hp = round_up(H, 64);
+        Lr = round_up(L, kSmLabelTile);
+        const int64_t most = (256LL << 20) / (2 * Bp) / kSmLabelTile * kSmLabelTile;
+        want = balanced(most < kSmLabelTile ? kSmLabelTile : most);
+        // two workgroups per CU for the feature gradient: label ranges of at
+        // least 128 labels whose partials are added afterwards
+        const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / kSmRowTile);
+        int64_t s = 512 / tiles;
+        if (s > want / 128) s = want / 128;
+        splits = (int)(s < 1 ? 1 : s);
+        size_t at = 0;
+        auto take = [&](size_t n) {
+            const size_t o = at;
+            at += align256(n);
+            return o;
+        };
+        nv = take(4);
+        rows = take((size_t)Bp * 4);
+        rank = take((size_t)B * 4);
+        hit = take((size_t)Bp * 4);
+        clse = take((size_t)Bp * 4);
+        part = take((size_t)(Lr / kSmLabelTile) * (size_t)Bp * 8);
+        hc = take((size_t)Bp * (size_t)Hp * 2);
+        dhp = grad ? take((size_t)splits * (size_t)Bp * (size_t)Hp * 4) : at;
+        dz = at;
+    }
+    int64_t balanced(int64_t most) const
+    {
+        const int64_t n = (Lr + most - 1) / most;
+        return round_up((Lr + n - 1) / n, kSmLabelTile);
+    }
+    size_t total(int64_t Lc, bool grad) const { return dz + (grad ? (size_t)Bp * (size_t)Lc * 2 : 0); }
+};
+
+int check_softmax_shape(int64_t B, int64_t H, int64_t L)
+{
+    if (B < 1 || H < 1 || L < 1) return HASTE_ERR_DIM;
+    if (H % 8 != 0 || H > 16384 || B > (1 << 20) || L > kMaxLabels) return HASTE_ERR_UNSUPPORTED;
+    // one workgroup per (label tile, row tile)
+    if (round_up(L, kSmLabelTile) / kSmLabelTile * (round_up(B, kSmRowTile) / kSmRowTile) >= (1LL << 31))
+        return HASTE_ERR_UNSUPPORTED;
+    return HASTE_OK;
+}
+
+int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
+                 void* dW, void* dh, float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L,
+                 int64_t ldh, int64_t ldw, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!h || !W || !y_rowptr || !y_col || !row_loss || !lse || !loss || (grad && (!dW || !dh)))
+        return HASTE_ERR_NULL;
+    if (!std::isfinite(scale) || ldh < H || ldw < H) return HASTE_ERR_DIM;
+    HASTE_TRY(check_softmax_shape(B, H, L));
+    if ((dtype != HASTE_BF16 && dtype != HASTE_F16) || ldh % 8 != 0 || ldw % 8 != 0 || ldh > (1LL << 30) ||
+        ldw > (1LL << 30))
+        return HASTE_ERR_UNSUPPORTED;
+    const void* const all[] = {h, W, y_rowptr, y_col, row_loss, lse, loss, dW, dh};
+    for (const void* p : all)
+        if (!aligned16(p)) return HASTE_ERR_ALIGN;
+    const SoftmaxLayout l(B, H, L, grad);
+    HASTE_TRY(check_ws(workspace, workspace_bytes, l.total(kSmLabelTile, grad)));
+    char* const w = (char*)workspace;
+    SoftmaxArgs a{};
+    a.h = h; a.W = W; a.y_rowptr = y_rowptr; a.y_col = y_col;
+    a.B = B; a.H = H; a.L = L; a.ldh = ldh; a.ldw = ldw; a.scale = scale;
+    a.dW = dW; a.dh = dh; a.row_loss = row_loss; a.lse = lse; a.loss = loss;
+    a.Bp = l.Bp; a.Hp = l.Hp; a.splits = l.splits;
+    a.Lc = l.want;
+    if (grad && workspace_bytes < l.total(l.want, true))
+        a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / (2 * (size_t)l.Bp)) / kSmLabelTile * kSmLabelTile);
+    a.nv = (int32_t*)(w + l.nv);
+    a.rows = (int32_t*)(w + l.rows);
+    a.rank = (int32_t*)(w + l.rank);
+    a.hit = (float*)(w + l.hit);
+    a.clse = (float*)(w + l.clse);
+    a.part = (float*)(w + l.part);
+    a.hc = (uint16_t*)(w + l.hc);
+    a.dhp = (float*)(w + l.dhp);
+    a.dz = (uint16_t*)(w + l.dz);
+    launch_softmax(dtype, grad, a, stream);
+    return hip_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+int haste_dropout(const void* x, const void* residual, void* y, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                  double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype, hipStream_t stream)
+{
+    if (!x || !y) return HASTE_ERR_NULL;
+    HASTE_TRY(check_rows(rows, cols, ldx, ldr, residual != nullptr, dtype));
+    const size_t e = elem_size(dtype);
+    if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned16(y)) return HASTE_ERR_ALIGN;
+    Drop d;
+    HASTE_TRY(make_drop(p, seed, offset, offset_dev, d));
+    launch_dropout(dtype, DropoutArgs{x, residual, y, rows, cols, ldx, ldr}, d, stream);
+    return hip_status();
+}
+
+int haste_add_norm(const void* x, const void* residual, const void* gamma, void* sum, void* y, uint8_t* q,
+                   float* q_scale, float* rstd, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps,
+                   double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype,
+                   hipStream_t stream)
+{
+    if (!x || !gamma || (!y && !q) || (q && !q_scale)) return HASTE_ERR_NULL;
+    HASTE_TRY(check_rows(rows, cols, ldx, ldr, residual != nullptr, dtype));
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return HASTE_ERR_DIM;
+    if (cols > kNormMaxCols || rows >= (1LL << 31)) return HASTE_ERR_UNSUPPORTED;
+    const size_t e = elem_size(dtype);
+    if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned16(gamma) || !aligned16(sum) || !aligned16(y) ||
+        !aligned16(q) || !aligned16(q_scale) || !aligned16(rstd))
+        return HASTE_ERR_ALIGN;
+    Drop d;
+    HASTE_TRY(make_drop(p, seed, offset, offset_dev, d));
+    launch_add_norm(dtype, NormArgs{x, residual, gamma, sum, y, q, q_scale, rstd, rows, cols, ldx, ldr, eps}, d,
+                    stream);
+    return hip_status();
+}
+
+size_t haste_add_norm_workspace_size(int64_t rows, int64_t cols)
+{
+    if (rows < 1 || cols < 1 || cols > kNormMaxCols) return 0;
+    return align256((size_t)norm_bwd_groups(rows, cols) * (size_t)cols * 4);
+}
+
+int haste_add_norm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
+                       void* dres, void* dx, float* dgamma, int64_t rows, int64_t cols, int64_t lddy, int64_t ldds,
+                       double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!dy || !sum || !gamma || !rstd || !dres) return HASTE_ERR_NULL;
+    HASTE_TRY(check_rows(rows, cols, lddy, ldds, dsum != nullptr, dtype));
+    if (cols > kNormMaxCols || rows >= (1LL << 31)) return HASTE_ERR_UNSUPPORTED;
+    const size_t e = elem_size(dtype);
+    if (!aligned_to(dy, e) || !aligned_to(dsum, e) || !aligned16(sum) || !aligned16(gamma) || !aligned16(rstd) ||
+        !aligned16(dres) || !aligned16(dx) || !aligned16(dgamma))
+        return HASTE_ERR_ALIGN;
+    Drop d;
+    HASTE_TRY(make_drop(p, seed, offset, offset_dev, d));
+    if (dgamma) HASTE_TRY(check_ws(workspace, workspace_bytes, haste_add_norm_workspace_size(rows, cols)));
+    launch_add_norm_bwd(dtype,
+                        NormBwdArgs{dy, sum, gamma, rstd, dsum, dres, dx, dgamma,
+                                    dgamma ? (float*)workspace : nullptr, rows, cols, lddy, ldds},
+                        d, stream);
+    return hip_status();
+}
+
+int haste_quantize_rows(const void* x, uint8_t* q, float* scale, int64_t rows, int64_t cols, int64_t ldx, int dtype,
+                        hipStream_t stream)
+{
+    if (!x || !q || !scale) return HASTE_ERR_NULL;
+    HASTE_TRY(check_rows(rows, cols, ldx, 0, false, dtype));
+    if (cols > kNormMaxCols || rows >= (1LL << 31)) return HASTE_ERR_UNSUPPORTED;
+    if (!aligned_to(x, elem_size(dtype)) || !aligned16(q) || !aligned16(scale)) return HASTE_ERR_ALIGN;
+    launch_quantize_rows(dtype, x, ldx, rows, cols, q, scale, stream);
+    return hip_status();
+}
+
+int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq, const float* w_scale, float* Z,
+                     int64_t B, int64_t H, int64_t L, hipStream_t stream)
+{
+    if (!hq || !h_scale || !Wq || !w_scale || !Z) return HASTE_ERR_NULL;
+    if (B < 1 || H < 1 || L < 1) return HASTE_ERR_DIM;
+    if (H % 16 != 0 || H > 16384 || L > kMaxLabels || B > (1 << 20)) return HASTE_ERR_UNSUPPORTED;
+    if (!aligned16(hq) || !aligned16(h_scale) || !aligned16(Wq) || !aligned16(w_scale) || !aligned16(Z))
+        return HASTE_ERR_ALIGN;
+    launch_score(ScoreArgs{hq, h_scale, Wq, w_scale, Z, B, H, L}, stream);
+    return hip_status();
+}
+
+size_t haste_softmax_workspace_size(int64_t B, int64_t H, int64_t L, int grad)
+{
+    if (check_softmax_shape(B, H, L) != HASTE_OK) return 0;
+    const SoftmaxLayout l(B, H, L, grad != 0);
+    return l.total(l.want, grad != 0);
+}
+
+size_t haste_softmax_workspace_min(int64_t B, int64_t H, int64_t L, int grad)
+{
+    if (check_softmax_shape(B, H, L) != HASTE_OK) return 0;
+    return SoftmaxLayout(B, H, L, grad != 0).total(kSmLabelTile, grad != 0);
+}
+
+int haste_softmax_loss(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
+                       float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L, int64_t ldh,
+                       int64_t ldw, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return softmax_impl(false, h, W, y_rowptr, y_col, scale, nullptr, nullptr, row_loss, lse, loss, B, H, L, ldh, ldw,
+                        dtype, workspace, workspace_bytes, stream);
+}
+
+int haste_softmax_step(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
+                       void* dW, void* dh, float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L,
+                       int64_t ldh, int64_t ldw, int dtype, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream)
+{
+    return softmax_impl(true, h, W, y_rowptr, y_col, scale, dW, dh, row_loss, lse, loss, B, H, L, ldh, ldw, dtype,
+                        workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "api_util.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -20,10 +21,6 @@ constexpr int64_t kMaxLabels = 2147483647LL - 64;
 // Bound of the feature-gradient turn waits; only haste_test_set_turn_spins
 // changes it (to force the give-up path in tests).
 std::atomic<int> g_turn_spins{kTurnSpins};
-
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 struct Layout {
     int64_t Bp;          // batch padded to 32 (feature-major copy of h)
@@ -113,18 +110,6 @@ int check_shape(int64_t B, int64_t H, int64_t K, int64_t G, int64_t F, bool fixe
     return HASTE_OK;
 }
 
-int check_ws(void* ws, size_t ws_bytes, size_t need)
-{
-    if (need == 0) return HASTE_OK;
-    if (ws == nullptr || ws_bytes < need || ((uintptr_t)ws & 255u) != 0) return HASTE_ERR_WORKSPACE;
-    return HASTE_OK;
-}
-
-int hip_status()
-{
-    return hipGetLastError() == hipSuccess ? HASTE_OK : HASTE_ERR_HIP;
-}
-
 int fwd_grid(int64_t K)
 {
     int64_t g = (K + 3) / 4;
@@ -134,16 +119,6 @@ int fwd_grid(int64_t K)
 }  // namespace
 
 int haste::turn_spins() { return g_turn_spins.load(std::memory_order_relaxed); }
-
-namespace {
-
-#define HASTE_TRY(x)                 \
-    do {                             \
-        int _st = (x);               \
-        if (_st != HASTE_OK) return _st; \
-    } while (0)
-
-}  // namespace
 
 extern "C" {
 

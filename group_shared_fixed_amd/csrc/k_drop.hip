@@ -1,0 +1,55 @@
+// Dropout with an optional residual: y = residual + dropout(x).
+//
+// The mask comes from a counter-based generator (elem.hpp) and is never
+// stored: the backward pass is the same call on the upstream gradient.
+// One thread per eight consecutive elements of a row.
+#include "elem.hpp"
+#include "kernels.hpp"
+
+namespace haste {
+namespace {
+
+template <int DT, bool RES>
+__global__ __launch_bounds__(256) void k_dropout(DropoutArgs a, Drop d)
+{
+    const int64_t per = (a.cols + 7) / 8, n = a.rows * per;
+    const Philox g = drop_generator(d);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = n <= 0xffffffffLL ? (int64_t)((uint32_t)i / (uint32_t)per) : i / per;
+        const int64_t c = 8 * (i - row * per), left = a.cols - c;
+        const Raw8<DT> x = load8<DT>(a.x, row * a.ldx + c, left);
+        Raw8<DT> r;
+        if constexpr (RES) r = load8<DT>(a.residual, row * a.ldr + c, left);
+        float v[8];
+        widen8<DT>(x, v);
+        if (d.thr) drop8(d, g, (uint64_t)i, v);
+        if constexpr (RES) {
+            float w[8];
+            widen8<DT>(r, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+        store8<DT>(a.y, row * a.cols + c, left, v);
+    }
+}
+
+template <int DT>
+void launch(const DropoutArgs& a, const Drop& d, hipStream_t s)
+{
+    const int64_t n = a.rows * ((a.cols + 7) / 8);
+    const int64_t grid = (n + 255) / 256;
+    const unsigned g = (unsigned)(grid > (1 << 20) ? (1 << 20) : grid);
+    if (a.residual) k_dropout<DT, true><<<g, 256, 0, s>>>(a, d);
+    else k_dropout<DT, false><<<g, 256, 0, s>>>(a, d);
+}
+
+}  // namespace
+
+void launch_dropout(int dtype, const DropoutArgs& a, const Drop& d, hipStream_t s)
+{
+    if (dtype == HASTE_BF16) launch<HASTE_BF16>(a, d, s);
+    else if (dtype == HASTE_F16) launch<HASTE_F16>(a, d, s);
+    else launch<HASTE_F32>(a, d, s);
+}
+
+}  // namespace haste

@@ -1,0 +1,336 @@
+// Root-mean-square norm with the residual's addition, forward and backward.
+//
+// Forward, per row: v = residual + dropout(x), rstd = 1 / sqrt(mean v^2 + eps),
+// y = v rstd gamma; y goes out in the input's type, or as E4M3 codes of
+// y / scale with one fp32 scale = max |y| / 448 per row, or both.  v is kept
+// in fp32 registers from its formation to the codes, so the rounded sum that
+// is stored for later layers never enters this row's statistics.
+//
+// Backward, per row, from the stored sum v and rstd: with xh = v rstd and
+// g = dy gamma, ds = rstd (g - xh mean(g xh)) + dsum; dx = dropout mask of
+// ds; dgamma = sum over rows of dy xh (fp32 partial sums per workgroup,
+// added in a fixed order by a second kernel: bitwise repeatable).
+//
+// Both are bound by memory: every row is read once, into registers.
+#include "elem.hpp"
+#include "kernels.hpp"
+
+namespace haste {
+namespace {
+
+// Sum (or maximum) over the T threads that share a row; every thread gets it.
+template <int T, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* sh)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        const float u = __shfl_xor(v, o, 64);
+        v = MAX ? fmaxf(v, u) : v + u;
+    }
+    if constexpr (T > 64) {
+        constexpr int NW = T / 64;
+        __syncthreads();                      // sh may still be read for the previous value
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = sh[0];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) v = MAX ? fmaxf(v, sh[w]) : v + sh[w];
+    }
+    return v;
+}
+
+// T threads per row, NV blocks of eight elements per thread.
+template <int DT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop d)
+{
+    constexpr int RPB = T < 256 ? 256 / T : 1;
+    __shared__ float sh[16];
+    const int t = T < 256 ? (int)threadIdx.x % T : (int)threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * RPB + (T < 256 ? threadIdx.x / T : 0);
+    if (row >= a.rows) return;                // whole waves; T > 64 has one row per workgroup
+    const int64_t per = (a.cols + 7) / 8;
+
+    Raw8<DT> rx[NV], rr[NV], rg[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T, c = 8 * b;
+        if (b < per) {
+            rx[k] = load8<DT>(a.x, row * a.ldx + c, a.cols - c);
+            if (a.residual) rr[k] = load8<DT>(a.residual, row * a.ldr + c, a.cols - c);
+            rg[k] = load8<DT>(a.gamma, c, a.cols - c);
+        }
+    }
+    const Philox g = drop_generator(d);
+    float v[NV][8], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+        if (b < per) {
+            widen8<DT>(rx[k], v[k]);
+            if (d.thr) drop8(d, g, (uint64_t)(row * per + b), v[k]);
+            if (a.residual) {
+                float w[8];
+                widen8<DT>(rr[k], w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+            }
+            if (a.sum) store8<DT>(a.sum, row * a.cols + 8 * b, a.cols - 8 * b, v[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += v[k][e] * v[k][e];
+        }
+    }
+    ss = row_reduce<T, false>(ss, sh);
+    const float rstd = 1.0f / sqrtf(ss / (float)a.cols + a.eps);
+    if (a.rstd && t == 0) a.rstd[row] = rstd;
+
+    float top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+        if (b < per) {
+            float w[8];
+            widen8<DT>(rg[k], w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[k][e] = v[k][e] * rstd * w[e];
+                top = fmaxf(top, fabsf(v[k][e]));
+            }
+            if (a.y) store8<DT>(a.y, row * a.cols + 8 * b, a.cols - 8 * b, v[k]);
+        }
+    }
+    if (a.q) {
+        top = row_reduce<T, true>(top, sh);
+        if (t == 0) a.q_scale[row] = top / 448.0f;
+        const float inv = top > 0.f ? 448.0f / top : 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t b = t + (int64_t)k * T;
+            if (b < per) store_e4m3(a.q, row * a.cols + 8 * b, a.cols - 8 * b, v[k], inv);
+        }
+    }
+}
+
+// E4M3 rows with one scale of x as it is (the operand format of the scoring
+// call, for weights and for features that need no norm).
+template <int DT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_quantize_rows(const void* x, int64_t ldx, int64_t rows,
+                                                                     int64_t cols, uint8_t* q, float* scale)
+{
+    constexpr int RPB = T < 256 ? 256 / T : 1;
+    __shared__ float sh[16];
+    const int t = T < 256 ? (int)threadIdx.x % T : (int)threadIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * RPB + (T < 256 ? threadIdx.x / T : 0);
+    if (row >= rows) return;
+    const int64_t per = (cols + 7) / 8;
+    float v[NV][8], top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+        if (b < per) {
+            widen8<DT>(load8<DT>(x, row * ldx + 8 * b, cols - 8 * b), v[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[k][e]));
+        }
+    }
+    top = row_reduce<T, true>(top, sh);
+    if (t == 0) scale[row] = top / 448.0f;
+    const float inv = top > 0.f ? 448.0f / top : 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+        if (b < per) store_e4m3(q, row * cols + 8 * b, cols - 8 * b, v[k], inv);
+    }
+}
+
+// Workgroup w takes rows w RPB + r, w RPB + r + gridDim.x RPB, ...; its
+// partial of dgamma goes to part[w].
+template <int DT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs a, Drop d)
+{
+    constexpr int RPB = T < 256 ? 256 / T : 1;
+    constexpr int NB = T < 256 ? T : 1;
+    __shared__ float sh[16];
+    __shared__ float acc[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? NV * NB * 8 : 1];
+    const int t = T < 256 ? (int)threadIdx.x % T : (int)threadIdx.x;
+    const int r0 = T < 256 ? (int)threadIdx.x / T : 0;
+    const int64_t per = (a.cols + 7) / 8;
+    const float inv_n = 1.0f / (float)a.cols;
+    const Philox g = drop_generator(d);
+
+    float gm[NV][8], dg[NV][8];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gm[k][e] = dg[k][e] = 0.f;
+        if (b < per) widen8<DT>(load8<DT>(a.gamma, 8 * b, a.cols - 8 * b), gm[k]);
+    }
+    for (int64_t row = (int64_t)blockIdx.x * RPB + r0; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+        Raw8<DT> ry[NV], rs[NV], rd[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t b = t + (int64_t)k * T, c = 8 * b;
+            if (b < per) {
+                ry[k] = load8<DT>(a.dy, row * a.lddy + c, a.cols - c);
+                rs[k] = load8<DT>(a.sum, row * a.cols + c, a.cols - c);
+                if (a.dsum) rd[k] = load8<DT>(a.dsum, row * a.ldds + c, a.cols - c);
+            }
+        }
+        const float rstd = a.rstd[row];
+        float dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (t + (int64_t)k * T < per) {
+                float dy[8], xh[8];
+                widen8<DT>(ry[k], dy);
+                widen8<DT>(rs[k], xh);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float p = dy[e] * (xh[e] * rstd);
+                    dot += p * gm[k][e];
+                    dg[k][e] += p;
+                }
+            }
+        }
+        dot = row_reduce<T, false>(dot, sh);
+        const float c0 = dot * inv_n;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t b = t + (int64_t)k * T;
+            if (b < per) {
+                float dy[8], xh[8], ds[8];
+                widen8<DT>(ry[k], dy);
+                widen8<DT>(rs[k], xh);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ds[e] = (dy[e] * gm[k][e] - xh[e] * rstd * c0) * rstd;
+                if (a.dsum) {
+                    float w[8];
+                    widen8<DT>(rd[k], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ds[e] += w[e];
+                }
+                store8<DT>(a.dres, row * a.cols + 8 * b, a.cols - 8 * b, ds);
+                if (a.dx) {
+                    if (d.thr) drop8(d, g, (uint64_t)(row * per + b), ds);
+                    store8<DT>(a.dx, row * a.cols + 8 * b, a.cols - 8 * b, ds);
+                }
+            }
+        }
+    }
+    if (!a.part) return;
+    // the rows of the workgroup's other threads groups join the first's
+    if constexpr (RPB > 1) {
+        if (r0 > 0) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[r0 - 1][(k * 8 + e) * NB + t] = dg[k][e];
+        }
+        __syncthreads();
+        if (r0 > 0) return;
+#pragma unroll
+        for (int r = 0; r < RPB - 1; ++r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dg[k][e] += acc[r][(k * 8 + e) * NB + t];
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t b = t + (int64_t)k * T;
+        if (b < per) store8<HASTE_F32>(a.part, (int64_t)blockIdx.x * a.cols + 8 * b, a.cols - 8 * b, dg[k]);
+    }
+}
+
+// out[j] = sum over i < n of part[i][j], i in 16 interleaved sequences that
+// are then added in order: one workgroup per 16 columns.
+__global__ __launch_bounds__(256) void k_column_sum(const float* part, int64_t n, int64_t cols, float* out)
+{
+    __shared__ float sh[16][17];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t j = (int64_t)blockIdx.x * 16 + c;
+    float s = 0.f;
+    if (j < cols) {
+#pragma unroll 8
+        for (int64_t i = r; i < n; i += 16) s += part[i * cols + j];
+    }
+    sh[r][c] = s;
+    __syncthreads();
+    if (r == 0 && j < cols) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += sh[k][c];
+        out[j] = s;
+    }
+}
+
+// Threads per row: one wave up to 1024 columns (no barriers, four rows per
+// workgroup), 256 up to 8192, 1024 beyond.
+template <typename F>
+void by_width(int64_t cols, F&& f)
+{
+    const int64_t per = (cols + 7) / 8;
+    if (per <= 64) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    else if (per <= 128) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    else if (per <= 256) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    else if (per <= 512) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    else if (per <= 1024) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+
+template <typename F>
+void by_type(int dtype, F&& f)
+{
+    if (dtype == HASTE_BF16) f(std::integral_constant<int, HASTE_BF16>{});
+    else if (dtype == HASTE_F16) f(std::integral_constant<int, HASTE_F16>{});
+    else f(std::integral_constant<int, HASTE_F32>{});
+}
+
+unsigned row_groups(int64_t rows, int t) { return (unsigned)(t < 256 ? (rows * t + 255) / 256 : rows); }
+
+}  // namespace
+
+void launch_add_norm(int dtype, const NormArgs& a, const Drop& d, hipStream_t s)
+{
+    by_type(dtype, [&](auto dt) {
+        by_width(a.cols, [&](auto t, auto nv) {
+            constexpr int T = decltype(t)::value;
+            k_add_norm<decltype(dt)::value, T, decltype(nv)::value>
+                <<<row_groups(a.rows, T), T < 256 ? 256 : T, 0, s>>>(a, d);
+        });
+    });
+}
+
+void launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, float* scale,
+                          hipStream_t s)
+{
+    by_type(dtype, [&](auto dt) {
+        by_width(cols, [&](auto t, auto nv) {
+            constexpr int T = decltype(t)::value;
+            k_quantize_rows<decltype(dt)::value, T, decltype(nv)::value>
+                <<<row_groups(rows, T), T < 256 ? 256 : T, 0, s>>>(x, ldx, rows, cols, q, scale);
+        });
+    });
+}
+
+// Enough workgroups to keep every CU's memory queues full, few enough that
+// the dgamma partials stay small next to the rows themselves.
+int64_t norm_bwd_groups(int64_t rows, int64_t cols)
+{
+    const int64_t want = cols <= 1024 ? (rows + 3) / 4 : rows;
+    return want < 1024 ? want : 1024;
+}
+
+void launch_add_norm_bwd(int dtype, const NormBwdArgs& a, const Drop& d, hipStream_t s)
+{
+    const int64_t n = norm_bwd_groups(a.rows, a.cols);
+    by_type(dtype, [&](auto dt) {
+        by_width(a.cols, [&](auto t, auto nv) {
+            constexpr int T = decltype(t)::value;
+            k_add_norm_bwd<decltype(dt)::value, T, decltype(nv)::value>
+                <<<(unsigned)n, T < 256 ? 256 : T, 0, s>>>(a, d);
+        });
+    });
+    if (a.part) k_column_sum<<<(unsigned)((a.cols + 15) / 16), 256, 0, s>>>(a.part, n, a.cols, a.dgamma);
+}
+
+}  // namespace haste

@@ -1,0 +1,471 @@
+// Softmax cross entropy over a dense label matrix, with its gradient.
+//
+// For rows b with labels Y_b (m_b of them), z = h W^T and
+// lse_b = log sum_l exp z_bl:
+//   row_loss_b = lse_b - (1 / m_b) sum_{l in Y_b} z_bl
+//   D = softmax(z) - [l in Y_b] / m_b,  dW = s D^T h,  dh = s D W.
+// The logits are never kept: a first pass forms them tile by tile and keeps
+// one (maximum, sum) pair per row and 256-label tile; a second pass forms
+// them again, piece of the label space by piece, as D in the workspace (two
+// bytes per entry, Bp x Lc), from which the two gradient products of the
+// piece are taken.  That is eight instead of six B L H operations, against
+// four bytes per logit written and read twice.
+//
+// Rows without labels are left out: the rows that have some are compacted
+// first (ranks), so padding costs no products and nothing in a padded row
+// (NaN included) reaches a result.
+//
+// D is rounded to the operands' type for the matrix cores: half a step of
+// relative error per entry, the size of the rounding of dW and dh
+// themselves; in fp16 it is held times 2^12, since probabilities of 1e-5
+// would be subnormal there.
+#include "elem.hpp"
+#include "kernels.hpp"
+
+namespace haste {
+namespace {
+
+constexpr int kTM = (int)kSmLabelTile;   // 256
+constexpr int kTN = (int)kSmRowTile;     // 128
+constexpr int kStage = 32;               // contraction per LDS stage
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// 32x32x16 product, fp32 accumulate.  Lane l supplies A row (l % 32) and B
+// column (l % 32), contraction elements 8 (l / 32) .. + 8; lane l holds
+// column (l % 32), element e at row 8 (e / 4) + 4 (l / 32) + e % 4.
+template <int DT>
+__device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c)
+{
+    if constexpr (DT == HASTE_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b),
+                                                      c, 0, 0, 0);
+}
+
+// D is held times this in the workspace.
+template <int DT>
+constexpr float kDScale = DT == HASTE_F16 ? 4096.0f : 1.0f;
+
+// rows / rank / nv: the ranks of the rows that have labels, in row order.
+__global__ __launch_bounds__(1024) void k_sm_rows(const int32_t* __restrict__ rowptr, int64_t B, int64_t Bp,
+                                                  int32_t* __restrict__ rows, int32_t* __restrict__ rank,
+                                                  int32_t* __restrict__ nv)
+{
+    __shared__ int32_t cnt[1024];
+    const int t = threadIdx.x;
+    const int64_t per = (B + 1023) / 1024, b0 = t * per, b1 = b0 + per < B ? b0 + per : B;
+    int n = 0;
+    for (int64_t b = b0; b < b1; ++b) n += rowptr[b + 1] > rowptr[b];
+    cnt[t] = n;
+    __syncthreads();
+    for (int o = 1; o < 1024; o <<= 1) {
+        const int v = t >= o ? cnt[t - o] : 0;
+        __syncthreads();
+        cnt[t] += v;
+        __syncthreads();
+    }
+    int at = cnt[t] - n;
+    for (int64_t b = b0; b < b1; ++b) {
+        const bool has = rowptr[b + 1] > rowptr[b];
+        rank[b] = has ? at : -1;
+        if (has) rows[at++] = (int32_t)b;
+    }
+    if (t == 1023) *nv = cnt[1023];
+}
+
+// <hc[i], W[l]> by one wave, fp32.
+template <int DT>
+__device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* hrow, int64_t l, int lane)
+{
+    float s = 0.f;
+    for (int64_t j = 8 * lane; j < a.H; j += 512) {
+        float x[8], w[8];
+        widen8<DT>(load8<DT>(hrow, j, 8), x);
+        widen8<DT>(load8<DT>(a.W, l * a.ldw + j, 8), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += x[e] * w[e];
+    }
+    return wave_sum(s);
+}
+
+// Workgroup i: row of rank i into hc (zeros past nv and past H), and the
+// mean logit of its labels.
+template <int DT>
+__global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
+{
+    __shared__ float sh[4];
+    const int64_t i = blockIdx.x;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const bool live = i < *a.nv;
+    const int64_t b = live ? a.rows[i] : 0;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.h) + b * a.ldh;
+    for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048)
+        *reinterpret_cast<u32x4_t*>(a.hc + i * a.Hp + j) =
+            live && j < a.H ? ldg16(src + j) : u32x4_t{0u, 0u, 0u, 0u};
+    if (!live) return;
+    const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
+    float s = 0.f;
+    for (int p = p0 + w; p < p1; p += 4) {
+        const int64_t l = a.y_col[p];
+        if (l >= 0 && l < a.L) s += wave_dot<DT>(a, src, l, lane);
+    }
+    if (lane == 0) sh[w] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) a.hit[i] = ((sh[0] + sh[1]) + (sh[2] + sh[3])) / (float)(p1 - p0);
+}
+
+// An operand tile: T (256 or 128) tile rows by 32 contraction elements.
+// Contraction-contiguous operands (TR = false) lie in memory as one row of
+// `ld` elements per tile row; row-contiguous ones (TR = true) as one row of
+// ld elements per contraction index, with the tile rows along it.
+struct Operand {
+    const uint16_t* p;
+    int64_t ld;
+    int64_t rows;     // valid tile-row indices: [0, rows), past it the last one is read again
+    int64_t depth;    // valid contraction indices, likewise
+};
+
+// LDS images (16-byte pieces): TR = false: tile row r, piece c (of 4) at
+// 4 r + (c ^ (r / 4) % 4).  TR = true: contraction row k, piece c (of T / 8)
+// at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the pieces that one operand
+// read touches over the banks.
+template <int T, bool TR>
+__device__ __forceinline__ u32x4_t fetch_piece(const Operand& o, int64_t r0, int64_t k0, int u)
+{
+    int64_t r, k;
+    if constexpr (TR) {
+        const int row = u / (T / 8), c = (u % (T / 8)) ^ (4 * (row & 3));
+        k = k0 + row;
+        r = r0 + 8 * c;
+        const int64_t last = o.rows - 8;
+        r = r < last ? r : last;
+        k = k < o.depth ? k : o.depth - 1;
+        return ldg16(o.p + k * o.ld + r);
+    } else {
+        const int row = u / 4, c = (u % 4) ^ ((row >> 2) & 3);
+        r = r0 + row;
+        k = k0 + 8 * c;
+        r = r < o.rows ? r : o.rows - 1;
+        const int64_t last = o.depth - 8;
+        k = k < last ? k : last;
+        return ldg16(o.p + r * o.ld + k);
+    }
+}
+
+// Operand fragment of the 32 tile rows 32 x .., contraction step s (16 deep).
+template <int T, bool TR>
+__device__ __forceinline__ u32x4_t fragment(const uint16_t* tile, int x, int s, int lane)
+{
+    if constexpr (TR) {
+        const int g = lane >> 4, rr = (lane >> 2) & 3, cc = lane & 3;
+        const int piece = 4 * x + 2 * (g & 1) + (cc >> 1);
+        const uint16_t* p = tile + (16 * s + 8 * (g >> 1) + rr) * T + 8 * (piece ^ (4 * rr)) + 4 * (cc & 1);
+        return cat(lds_tr16(p), lds_tr16(p + 4 * T));
+    } else {
+        const int r = 32 * x + (lane & 31);
+        return *reinterpret_cast<const u32x4_t*>(tile + r * kStage + 8 * ((2 * s + (lane >> 5)) ^ ((r >> 2) & 3)));
+    }
+}
+
+// acc (4 x 2 tiles of 32 x 32 per wave; wave w: tile rows 128 (w / 2) ..,
+// columns 64 (w % 2) ..) += A B^T over contraction [k0, k1), whole stages.
+template <int DT, bool ATR, bool BTR>
+__device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t k0,
+                                             int64_t k1, uint16_t* sA, uint16_t* sB, f32x16_t (&acc)[4][2])
+{
+    const int tid = threadIdx.x, lane = tid & 63, wm = tid >> 7, wn = (tid >> 6) & 1;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = f32x16_t{};
+    for (int64_t k = k0; k < k1; k += kStage) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<u32x4_t*>(sA)[tid + 256 * i] = fetch_piece<kTM, ATR>(A, m0, k, tid + 256 * i);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            reinterpret_cast<u32x4_t*>(sB)[tid + 256 * i] = fetch_piece<kTN, BTR>(B, n0, k, tid + 256 * i);
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            u32x4_t bf[2];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) bf[nt] = fragment<kTN, BTR>(sB, 2 * wn + nt, s, lane);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                const u32x4_t af = fragment<kTM, ATR>(sA, 4 * wm + mt, s, lane);
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af, bf[nt], acc[mt][nt]);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Logits of one 256-label x 128-row tile.  GRAD = false: the tile's (maximum,
+// sum of exponentials) per row.  GRAD = true: D = exp(z - lse) of the piece
+// of labels [l0, l0 + Lc), without the labels' own terms.
+template <int DT, bool GRAD>
+__global__ __launch_bounds__(256, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
+    __shared__ float red[2][kTN][2];
+    const int64_t mt0 = blockIdx.x / (a.Bp / kTN), n0 = blockIdx.x % (a.Bp / kTN) * kTN;
+    const int nv = *a.nv;
+    if (n0 >= nv) return;
+    const int64_t m0 = l0 + mt0 * kTM;
+    const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
+    f32x16_t acc[4][2];
+    tile_product<DT, false, false>(A, m0, B, n0, 0, a.Hp, sA, sB, acc);
+
+    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+    const int hl = lane >> 5, r32 = lane & 31;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const int64_t n = n0 + 64 * wn + 32 * nt + r32;
+        if constexpr (!GRAD) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (m0 + 128 * wm + 32 * mt + 8 * (e >> 2) + 4 * hl + (e & 3) >= a.L) acc[mt][nt][e] = -INFINITY;
+                    top = fmaxf(top, acc[mt][nt][e]);
+                }
+            top = fmaxf(top, __shfl_xor(top, 32, 64));
+            float sum = 0.f;
+            const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f((acc[mt][nt][e] - base) * kLog2e);
+            sum += __shfl_xor(sum, 32, 64);
+            if (hl == 0) {
+                red[wm][64 * wn + 32 * nt + r32][0] = top;
+                red[wm][64 * wn + 32 * nt + r32][1] = sum;
+            }
+        } else {
+            const float lse = n < nv ? a.clse[n] : 0.f, f = n < nv ? kDScale<DT> : 0.f;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t m = mt0 * kTM + 128 * wm + 32 * mt + 8 * g + 4 * hl;
+                    float d[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        d[i] = l0 + m + i < a.L ? __builtin_amdgcn_exp2f((acc[mt][nt][4 * g + i] - lse) * kLog2e) * f
+                                                : 0.f;
+                    *reinterpret_cast<u32x2_t*>(a.dz + n * a.Lc + m) =
+                        u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
+                }
+        }
+    }
+    if constexpr (!GRAD) {
+        __syncthreads();
+        if (threadIdx.x < kTN) {
+            const float t0 = red[0][threadIdx.x][0], t1 = red[1][threadIdx.x][0];
+            const float top = fmaxf(t0, t1), base = top == -INFINITY ? 0.f : top;
+            const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f((t0 - base) * kLog2e) +
+                              red[1][threadIdx.x][1] * __builtin_amdgcn_exp2f((t1 - base) * kLog2e);
+            *reinterpret_cast<f32x2_t*>(a.part + 2 * (mt0 * a.Bp + n0 + threadIdx.x)) = f32x2_t{top, sum};
+        }
+    }
+}
+
+// Log-sum-exp of 16 ranks per workgroup from the tiles' pairs, 16 threads
+// per rank; the results by row (0 for rows without labels).
+__global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
+{
+    __shared__ float st[16][17], ss[16][17];
+    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int64_t i = (int64_t)blockIdx.x * 16 + c;
+    const int nv = *a.nv;
+    float top = -INFINITY, sum = 0.f;
+    if (i < nv) {
+        for (int64_t t = r; t < tiles; t += 16) {
+            const f32x2_t p = *reinterpret_cast<const f32x2_t*>(a.part + 2 * (t * a.Bp + i));
+            const float nt = fmaxf(top, p[0]), base = nt == -INFINITY ? 0.f : nt;
+            sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + p[1] * __builtin_amdgcn_exp2f((p[0] - base) * kLog2e);
+            top = nt;
+        }
+    }
+    st[r][c] = top;
+    ss[r][c] = sum;
+    __syncthreads();
+    if (r == 0 && i < nv) {
+        for (int k = 1; k < 16; ++k) top = fmaxf(top, st[k][c]);
+        const float base = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+        for (int k = 0; k < 16; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f((st[k][c] - base) * kLog2e);
+        const float lse = base + logf(sum);
+        a.clse[i] = lse;
+        a.lse[a.rows[i]] = lse;
+        a.row_loss[a.rows[i]] = lse - a.hit[i];
+    }
+    // rows without labels
+    if (threadIdx.x < 16) {
+        const int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x;
+        if (b < a.B && a.rank[b] < 0) a.lse[b] = a.row_loss[b] = 0.f;
+    }
+}
+
+// The labels' own entries of D in the piece [l0, l0 + Lc): one workgroup per
+// rank.  The logit is formed again here, in fp32.
+template <int DT>
+__global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
+{
+    const int64_t i = blockIdx.x;
+    if (i >= *a.nv) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t b = a.rows[i];
+    const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
+    const float share = 1.0f / (float)(p1 - p0), lse = a.clse[i];
+    for (int p = p0 + w; p < p1; p += 4) {
+        const int64_t l = a.y_col[p];
+        if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
+        const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
+        const float d = (__builtin_amdgcn_exp2f((z - lse) * kLog2e) - share) * kDScale<DT>;
+        if (lane == 0) a.dz[i * a.Lc + (l - l0)] = (uint16_t)pack2<DT>(d, 0.f);
+    }
+}
+
+// dW of one tile of 256 columns x 128 labels of the piece.
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
+    const int64_t m0 = (int64_t)(blockIdx.x % ncols) * kTM, n0 = (int64_t)(blockIdx.x / ncols) * kTN;
+    const int nv = *a.nv;
+    const Operand A{a.hc, a.Hp, a.Hp, a.Bp}, B{a.dz, a.Lc, a.Lc, a.Bp};
+    f32x16_t acc[4][2];
+    tile_product<DT, true, true>(A, m0, B, n0, 0, (nv + kStage - 1) / kStage * kStage, sA, sB, acc);
+    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+    const float f = a.scale / kDScale<DT>;
+    uint16_t* dW = reinterpret_cast<uint16_t*>(a.dW);
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const int64_t l = l0 + n0 + 64 * wn + 32 * nt + (lane & 31);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t j = m0 + 128 * wm + 32 * mt + 8 * g + 4 * (lane >> 5);
+                if (l < a.L && j < a.H)
+                    *reinterpret_cast<u32x2_t*>(dW + l * a.H + j) =
+                        u32x2_t{pack2<DT>(acc[mt][nt][4 * g] * f, acc[mt][nt][4 * g + 1] * f),
+                                pack2<DT>(acc[mt][nt][4 * g + 2] * f, acc[mt][nt][4 * g + 3] * f)};
+            }
+    }
+}
+
+// The piece's share of dh: 256 columns x 128 ranks over one of `splits`
+// ranges of its labels, added to (or, for the first piece, stored in) that
+// range's partial.
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
+    const int64_t nrows = a.Bp / kTN, s = blockIdx.x / (ncols * nrows), t = blockIdx.x % (ncols * nrows);
+    const int64_t m0 = (t % ncols) * kTM, n0 = t / ncols * kTN;
+    if (n0 >= *a.nv) return;
+    const int64_t len = (a.Lc / a.splits + kStage - 1) / kStage * kStage;
+    const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;       // labels of the piece
+    int64_t k0 = s * len, k1 = s == a.splits - 1 ? a.Lc : k0 + len;
+    if (k1 > (live + kStage - 1) / kStage * kStage) k1 = (live + kStage - 1) / kStage * kStage;
+    const Operand A{reinterpret_cast<const uint16_t*>(a.W) + l0 * a.ldw, a.ldw, a.H, live}, B{a.dz, a.Lc, a.Bp, a.Lc};
+    f32x16_t acc[4][2];
+    tile_product<DT, true, false>(A, m0, B, n0, k0, k1, sA, sB, acc);
+    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const int64_t n = n0 + 64 * wn + 32 * nt + (lane & 31);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t j = m0 + 128 * wm + 32 * mt + 8 * g + 4 * (lane >> 5);
+                if (j >= a.Hp) continue;
+                f32x4_t* o = reinterpret_cast<f32x4_t*>(a.dhp + (s * a.Bp + n) * a.Hp + j);
+                f32x4_t v = {acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2], acc[mt][nt][4 * g + 3]};
+                if (!first) v += *o;
+                *o = v;
+            }
+    }
+}
+
+// dh by row from the partials (0 for rows without labels); workgroup 0 also
+// adds up the loss, in 64 bits and a fixed order.
+template <int DT>
+__global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad)
+{
+    if (blockIdx.x == 0) {
+        __shared__ double sh[256];
+        double s = 0.0;
+        for (int64_t b = threadIdx.x; b < a.B; b += 256) s += (double)a.row_loss[b];
+        sh[threadIdx.x] = s;
+        __syncthreads();
+        for (int o = 128; o >= 1; o >>= 1) {
+            if ((int)threadIdx.x < o) sh[threadIdx.x] += sh[threadIdx.x + o];
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) *a.loss = (float)(sh[0] * (double)a.scale);
+        return;
+    }
+    if (!grad) return;
+    const int64_t per = a.H / 8, n = a.B * per;
+    const float f = a.scale / kDScale<DT>;
+    for (int64_t t = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; t < n; t += (int64_t)(gridDim.x - 1) * 256) {
+        const int64_t b = t / per, j = 8 * (t % per), i = a.rank[b];
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        if (i >= 0) {
+            for (int s = 0; s < a.splits; ++s) {
+                float w[8];
+                widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * a.Bp + i) * a.Hp + j, 8), w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += w[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= f;
+        store8<DT>(a.dh, b * a.H + j, 8, v);
+    }
+}
+
+template <int DT>
+void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
+{
+    const int64_t nrt = a.Bp / kTN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
+    k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
+    k_sm_gather<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a);
+    k_sm_logits<DT, false><<<(unsigned)(tiles * nrt), 256, 0, s>>>(a, 0);
+    k_sm_lse<<<(unsigned)((a.Bp + 15) / 16), 256, 0, s>>>(a, tiles);
+    if (grad) {
+        for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
+            const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
+            const int64_t lt = (live + kTM - 1) / kTM;
+            k_sm_logits<DT, true><<<(unsigned)(lt * nrt), 256, 0, s>>>(a, l0);
+            k_sm_labels<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a, l0);
+            k_sm_dw<DT><<<(unsigned)((live + kTN - 1) / kTN * ncols), 256, 0, s>>>(a, l0, ncols);
+            k_sm_dh<DT><<<(unsigned)(ncols * nrt * a.splits), 256, 0, s>>>(a, l0, ncols, l0 == 0);
+        }
+    }
+    const int64_t blocks = grad ? (a.B * (a.H / 8) + 255) / 256 : 0;
+    k_sm_finish<DT><<<(unsigned)(1 + (blocks > 4096 ? 4096 : blocks)), 256, 0, s>>>(a, grad);
+}
+
+}  // namespace
+
+void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s)
+{
+    if (dtype == HASTE_BF16) run<HASTE_BF16>(grad, a, s);
+    else run<HASTE_F16>(grad, a, s);
+}
+
+}  // namespace haste

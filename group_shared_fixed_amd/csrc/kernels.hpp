@@ -194,4 +194,89 @@ void run_group_greedy(const uint16_t* E, const int32_t* a, int64_t L, int64_t C,
                       uint64_t* keys, int32_t* start, int32_t* end, int32_t* gbase, int32_t* obase, int32_t* ngroups,
                       float* sim, uint8_t* taken, hipStream_t s);
 
+// Feature operators (elem.hpp, k_drop.hip, k_norm.hip, k_score.hip,
+// k_softmax.hip).  dtype: a haste_dtype.  Inputs with an ld may have strided
+// rows (in elements); outputs are contiguous.
+struct Drop;
+struct DropoutArgs {
+    const void* x;
+    const void* residual;   // nullable
+    void* y;
+    int64_t rows, cols, ldx, ldr;
+};
+void launch_dropout(int dtype, const DropoutArgs& a, const Drop& d, hipStream_t s);
+
+struct NormArgs {
+    const void* x;
+    const void* residual;   // nullable
+    const void* gamma;
+    void* sum;              // nullable
+    void* y;                // nullable
+    uint8_t* q;             // nullable, with q_scale
+    float* q_scale;
+    float* rstd;            // nullable
+    int64_t rows, cols, ldx, ldr;
+    float eps;
+};
+void launch_add_norm(int dtype, const NormArgs& a, const Drop& d, hipStream_t s);
+
+struct NormBwdArgs {
+    const void* dy;
+    const void* sum;
+    const void* gamma;
+    const float* rstd;
+    const void* dsum;       // nullable
+    void* dres;
+    void* dx;               // nullable
+    float* dgamma;          // nullable, with part (norm_bwd_groups x cols fp32)
+    float* part;
+    int64_t rows, cols, lddy, ldds;
+};
+constexpr int64_t kNormMaxCols = 32768;
+int64_t norm_bwd_groups(int64_t rows, int64_t cols);
+void launch_add_norm_bwd(int dtype, const NormBwdArgs& a, const Drop& d, hipStream_t s);
+void launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, float* scale,
+                          hipStream_t s);
+
+struct ScoreArgs {
+    const uint8_t* hq;      // B x H E4M3 codes
+    const float* hs;        // B scales
+    const uint8_t* Wq;      // L x H E4M3 codes
+    const float* ws;        // L scales
+    float* Z;               // B x L
+    int64_t B, H, L;
+};
+void launch_score(const ScoreArgs& a, hipStream_t s);
+
+// Softmax cross entropy over a dense label matrix.  Rows with labels are
+// compacted: rank i < nv is row rows[i].
+struct SoftmaxArgs {
+    const void* h;
+    const void* W;
+    const int32_t* y_rowptr;
+    const int32_t* y_col;
+    int64_t B, H, L, ldh, ldw;
+    float scale;
+    void* dW;               // L x H (gradient only)
+    void* dh;               // B x H (gradient only)
+    float* row_loss;        // B
+    float* lse;             // B
+    float* loss;            // 1
+    // workspace
+    int64_t Bp, Hp;         // B and H rounded up to kSmRowTile and 64
+    int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
+    int splits;             // label ranges of a piece's feature gradient
+    int32_t* nv;
+    int32_t* rows;          // Bp
+    int32_t* rank;          // B, -1 for rows without labels
+    float* hit;             // Bp: mean logit of the row's labels
+    float* clse;            // Bp: log-sum-exp by rank
+    float* part;            // label tiles x Bp x (max, sum)
+    uint16_t* hc;           // Bp x Hp
+    uint16_t* dz;           // Bp x Lc
+    float* dhp;             // splits x Bp x Hp
+};
+constexpr int64_t kSmLabelTile = 256, kSmRowTile = 128;
+void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s);
+
 }  // namespace haste

@@ -463,6 +463,105 @@ int haste_workspace_status(const void* workspace, int32_t* status, hipStream_t s
  * word reports it.  A negative value restores the default bound. */
 void haste_test_set_turn_spins(int spins);
 
+/* ------------------------------------------------------------------------
+ * Feature operators: what stands between an encoder block's output and the
+ * label space.  They take bf16, fp16 or (norm, dropout) fp32 arrays; every
+ * sum, norm, softmax statistic and product is held in fp32 and rounded once,
+ * to nearest even, where it is stored.  Inputs with an `ld` argument may have
+ * strided rows (ld elements apart, ld >= the row's length); outputs are
+ * contiguous.  Sizes below 1 return HASTE_ERR_DIM. */
+typedef enum {
+    HASTE_BF16 = 0,
+    HASTE_F16 = 1,
+    HASTE_F32 = 2
+} haste_dtype;
+
+/* Dropout with a counter-based mask: y = residual + keep(x), rows x cols.
+ * The eight elements 8c .. 8c + 7 of row r take the eight 16-bit halves (low
+ * half first) of the four words of Philox 4x32-10 at the counter words
+ * (i mod 2^32, i div 2^32, o mod 2^32, o div 2^32), i = r ceil(cols / 8) + c,
+ * o = offset (+ *offset_dev when offset_dev is given, modulo 2^64), under the
+ * key (seed mod 2^32, seed div 2^32).  An element is dropped when its half is
+ * below t = round(65536 p) and multiplied by 65536 / (65536 - t) otherwise;
+ * a dropped element contributes 0 whatever it holds, NaN included.  The mask
+ * depends on seed, offset and the position alone and is never stored: the
+ * gradient of x is the same call on the upstream gradient without a residual.
+ * offset_dev (nullable, device, 8-byte aligned) lets a captured graph draw
+ * new masks: it is read when the call runs.  0 <= p <= 1 (p = 1 drops
+ * everything).  residual is nullable; y may be x or residual if that has
+ * ld = cols.  x and residual aligned to their element, y to 16 bytes. */
+int haste_dropout(const void* x, const void* residual, void* y, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                  double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype, hipStream_t stream);
+
+/* Root-mean-square norm with the residual's addition, per row of cols:
+ *   v = residual + dropout(x)   (dropout as haste_dropout; p = 0: none)
+ *   rstd = 1 / sqrt(mean v^2 + eps),  y = v rstd gamma.
+ * Outputs, all but one of y and q nullable: sum = v in the input's type (the
+ * residual of the next block), y in the input's type, q = OCP E4M3 codes of
+ * y / q_scale with q_scale[row] = max |y| / 448 (fp32; 0 for a row of zeros,
+ * whose codes are 0), rstd (fp32, for the backward pass).  The statistics and
+ * both outputs come from the unrounded v.  gamma: cols values of the input's
+ * type.  residual is nullable; sum may be x or residual if that has
+ * ld = cols.  cols <= 32768.  x and residual aligned to their element, the
+ * others to 16 bytes. */
+int haste_add_norm(const void* x, const void* residual, const void* gamma, void* sum, void* y, uint8_t* q,
+                   float* q_scale, float* rstd, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps,
+                   double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype,
+                   hipStream_t stream);
+
+/* Its backward pass from dy, the forward's sum (contiguous) and rstd:
+ *   ds = rstd (g - xh mean(g xh)) + dsum,  g = dy gamma,  xh = sum rstd,
+ * dres = ds, dx = the forward's dropout mask applied to ds (nullable; equal
+ * to dres when p = 0), dgamma (nullable, fp32) = sum over rows of dy xh.
+ * dsum (nullable) is the gradient that reaches `sum` from later layers.
+ * Bitwise repeatable.  Workspace: haste_add_norm_workspace_size(rows, cols)
+ * bytes for the partial sums of dgamma (not used without it). */
+size_t haste_add_norm_workspace_size(int64_t rows, int64_t cols);
+int haste_add_norm_bwd(const void* dy, const void* sum, const void* gamma, const float* rstd, const void* dsum,
+                       void* dres, void* dx, float* dgamma, int64_t rows, int64_t cols, int64_t lddy, int64_t ldds,
+                       double p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, int dtype,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* x (rows x cols) as E4M3 codes with one scale per row, as haste_add_norm
+ * writes them: q = codes of x / scale, scale = max |x| / 448. */
+int haste_quantize_rows(const void* x, uint8_t* q, float* scale, int64_t rows, int64_t cols, int64_t ldx, int dtype,
+                        hipStream_t stream);
+
+/* Logits from 8-bit rows on both sides, the reader of haste_add_norm's codes:
+ * Z[b, l] = h_scale[b] w_scale[l] sum_j hq[b, j] Wq[l, j], Z B x L fp32, hq
+ * B x H and Wq L x H E4M3 codes (exact products, fp32 sums).  H % 16 == 0,
+ * L <= 2^31 - 65, B <= 2^20. */
+int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq, const float* w_scale, float* Z,
+                     int64_t B, int64_t H, int64_t L, hipStream_t stream);
+
+/* Softmax cross entropy over a dense label matrix W (L x H), with its
+ * gradient, without the B x L logits ever being kept.  Labels as CSR
+ * (y_rowptr, y_col); m_b = number of labels of row b:
+ *   z = h W^T, lse_b = log sum_l exp z_bl,
+ *   row_loss_b = lse_b - (1 / m_b) sum_{l in Y_b} z_bl,  loss = scale sum_b row_loss_b,
+ *   D = softmax(z) - [l in Y_b] / m_b,  dW = scale D^T h,  dh = scale D W.
+ * Rows without labels are padding: row_loss, lse and dh are 0 there, nothing
+ * they hold (NaN included) is used, and they cost no products.
+ * h (row stride ldh) and W (row stride ldw) are bf16 or fp16; dW (L x H) and
+ * dh (B x H) have their type; row_loss, lse (B) and loss (1) are fp32, loss
+ * summed in fp64.  D goes to the gradient products rounded to the operands'
+ * type.  haste_softmax_loss computes loss, row_loss and lse alone.
+ * All results are bitwise repeatable for one workspace size.
+ * H % 8 == 0, H <= 16384, ldh and ldw multiples of 8, B <= 2^20,
+ * L <= 2^31 - 65; pointers 16-byte aligned.
+ * Workspace: any size from haste_softmax_workspace_min (256 labels at a
+ * time) up; haste_softmax_workspace_size gives the size past which more does
+ * not help (pieces of up to 256 MiB of D).  `grad`: for haste_softmax_step. */
+size_t haste_softmax_workspace_size(int64_t B, int64_t H, int64_t L, int grad);
+size_t haste_softmax_workspace_min(int64_t B, int64_t H, int64_t L, int grad);
+int haste_softmax_loss(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
+                       float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L, int64_t ldh,
+                       int64_t ldw, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+int haste_softmax_step(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
+                       void* dW, void* dh, float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L,
+                       int64_t ldh, int64_t ldw, int dtype, void* workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 /* Static text for a haste_status value. */
 const char* haste_status_string(int status);
 
