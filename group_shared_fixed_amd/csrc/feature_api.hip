@@ -16,6 +16,7 @@ using namespace haste;
 namespace {
 
 constexpr int64_t kMaxLabels = 2147483647LL - 64;
+constexpr int64_t kMaxLd = 1LL << 22;          // a tile's 256 rows stay within 32-bit byte offsets
 constexpr int64_t kMaxRows = 1LL << 40;        // rows x cols stays far below 2^63
 
 inline bool aligned_to(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -104,8 +105,8 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
         return HASTE_ERR_NULL;
     if (!std::isfinite(scale) || ldh < H || ldw < H) return HASTE_ERR_DIM;
     HASTE_TRY(check_softmax_shape(B, H, L));
-    if ((dtype != HASTE_BF16 && dtype != HASTE_F16) || ldh % 8 != 0 || ldw % 8 != 0 || ldh > (1LL << 30) ||
-        ldw > (1LL << 30))
+    if ((dtype != HASTE_BF16 && dtype != HASTE_F16) || ldh % 8 != 0 || ldw % 8 != 0 || ldh > kMaxLd ||
+        ldw > kMaxLd)
         return HASTE_ERR_UNSUPPORTED;
     const void* const all[] = {h, W, y_rowptr, y_col, row_loss, lse, loss, dW, dh};
     for (const void* p : all)

@@ -128,32 +128,88 @@ struct Operand {
     int64_t depth;    // valid contraction indices, likewise
 };
 
-// LDS images (16-byte pieces): TR = false: tile row r, piece c (of 4) at
-// 4 r + (c ^ (r / 4) % 4).  TR = true: contraction row k, piece c (of T / 8)
-// at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the pieces that one operand
-// read touches over the banks.
-template <int T, bool TR>
-__device__ __forceinline__ u32x4_t fetch_piece(const Operand& o, int64_t r0, int64_t k0, int u)
+// s_waitcnt vmcnt(N) alone (expcnt and lgkmcnt at their no-wait maxima).
+template <int N>
+__device__ __forceinline__ void wait_moves()
 {
-    int64_t r, k;
-    if constexpr (TR) {
-        const int row = u / (T / 8), c = (u % (T / 8)) ^ (4 * (row & 3));
-        k = k0 + row;
-        r = r0 + 8 * c;
-        const int64_t last = o.rows - 8;
-        r = r < last ? r : last;
-        k = k < o.depth ? k : o.depth - 1;
-        return ldg16(o.p + k * o.ld + r);
-    } else {
-        const int row = u / 4, c = (u % 4) ^ ((row >> 2) & 3);
-        r = r0 + row;
-        k = k0 + 8 * c;
-        r = r < o.rows ? r : o.rows - 1;
-        const int64_t last = o.depth - 8;
-        k = k < last ? k : last;
-        return ldg16(o.p + r * o.ld + k);
-    }
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
+// Workgroup barrier without a memory fence (a fence would wait for every
+// move in flight); the empty asm statements keep the compiler from moving
+// memory accesses across it.
+__device__ __forceinline__ void stage_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// Moves of one operand tile from memory straight into LDS
+// (global_load_lds_dwordx4: a lane's 16 bytes land at the wave's LDS base +
+// 16 x lane).  LDS images in 16-byte pieces: TR = false: tile row r, piece
+// c (of 4) at 4 r + (c ^ (r / 4) % 4).  TR = true: contraction row k, piece
+// c (of T / 8) at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the pieces that
+// one operand read touches over the banks; since a lane's place in LDS is
+// fixed, the swizzle is in the piece it asks for.
+template <int T, bool TR>
+struct Mover {
+    static constexpr int N = T / 64;          // moves per wave and stage
+    const char* base;                         // tile's first row (TR: column), contraction index 0
+    uint32_t off[N];                          // byte offset of the lane's piece
+    int64_t step;                             // TR: bytes per stage
+    uint32_t row[N], pitch;                   // contraction index within the stage, bytes per row
+    int64_t depth;
+
+    __device__ __forceinline__ Mover(const Operand& o, int64_t r0, int wave, int lane)
+    {
+        depth = o.depth;
+        pitch = 2 * (uint32_t)o.ld;
+        if constexpr (TR) {
+            base = reinterpret_cast<const char*>(o.p);
+            step = 2 * kStage * o.ld;
+        } else {
+            base = reinterpret_cast<const char*>(o.p + r0 * o.ld);
+            step = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int u = 64 * (N * wave + i) + lane;
+            if constexpr (TR) {
+                const int k = u / (T / 8), c = (u % (T / 8)) ^ (4 * (k & 3));
+                int64_t r = r0 + 8 * c;
+                r = r < o.rows - 8 ? r : o.rows - 8;
+                row[i] = (uint32_t)k;
+                off[i] = 2 * (uint32_t)r;
+            } else {
+                const int r = u / 4, c = (u % 4) ^ ((r >> 2) & 3);
+                const int64_t last = o.rows - 1 - r0;
+                row[i] = 8 * (uint32_t)c;
+                off[i] = (uint32_t)(r < last ? r : last) * pitch;
+            }
+        }
+    }
+
+    // stage st into buf; pieces past the operand's depth repeat its last one
+    __device__ __forceinline__ void move(int64_t st, uint16_t* buf, int wave) const
+    {
+        const char* const b = TR ? base + st * step : base;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t o;
+            if constexpr (TR) {
+                const int64_t left = depth - st * kStage;
+                const uint32_t last = left < kStage ? (uint32_t)left - 1 : kStage - 1;
+                o = off[i] + (row[i] < last ? row[i] : last) * pitch;
+            } else {
+                const uint32_t k = (uint32_t)st * kStage + row[i], last = (uint32_t)depth - 8;
+                o = off[i] + 2 * (k < last ? k : last);
+            }
+            __builtin_amdgcn_global_load_lds(b + o, (lds_ptr)(buf + 512 * (N * wave + i)), 16, 0, 0);
+        }
+    }
+};
 
 // Operand fragment of the 32 tile rows 32 x .., contraction step s (16 deep).
 template <int T, bool TR>
@@ -170,40 +226,83 @@ __device__ __forceinline__ u32x4_t fragment(const uint16_t* tile, int x, int s, 
     }
 }
 
+// The stage ring: three buffers of both operands' tiles (72 KB: two
+// workgroups per CU).  Distinct objects, so that the compiler sees that an
+// operand read and a move in flight never meet and adds no waits.
+constexpr int kRing = (kTM + kTN) * kStage;
+#define HASTE_SM_RING                                              \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring0[kRing]; \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring1[kRing]; \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring2[kRing];
+
 // acc (4 x 2 tiles of 32 x 32 per wave; wave w: tile rows 128 (w / 2) ..,
-// columns 64 (w % 2) ..) += A B^T over contraction [k0, k1), whole stages.
+// columns 64 (w % 2) ..) += A B^T over nst stages of 32.  Per stage: wait for
+// this wave's moves of the stage (the next stage's stay in flight), one
+// barrier (everyone's moves are done, and the buffer read one stage ago is
+// free), the moves of the stage two ahead, the products.  On return no move
+// is in flight and the ring is free.
 template <int DT, bool ATR, bool BTR>
-__device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t k0,
-                                             int64_t k1, uint16_t* sA, uint16_t* sB, f32x16_t (&acc)[4][2])
+__device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t nst,
+                                             uint16_t* ring0, uint16_t* ring1, uint16_t* ring2, f32x16_t (&acc)[4][2])
 {
-    const int tid = threadIdx.x, lane = tid & 63, wm = tid >> 7, wn = (tid >> 6) & 1;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = f32x16_t{};
-    for (int64_t k = k0; k < k1; k += kStage) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<u32x4_t*>(sA)[tid + 256 * i] = fetch_piece<kTM, ATR>(A, m0, k, tid + 256 * i);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            reinterpret_cast<u32x4_t*>(sB)[tid + 256 * i] = fetch_piece<kTN, BTR>(B, n0, k, tid + 256 * i);
-        __syncthreads();
+    if (nst <= 0) return;
+    const Mover<kTM, ATR> ma(A, m0, w, lane);
+    const Mover<kTN, BTR> mb(B, n0, w, lane);
+    auto move = [&](int64_t st, uint16_t* buf) {
+        const int64_t s = st < nst ? st : nst - 1;       // past the end: into a buffer nobody reads
+        ma.move(s, buf, w);
+        mb.move(s, buf + kTM * kStage, w);
+    };
+    auto products = [&](const uint16_t* buf) {
+        const uint16_t* const tA = buf;
+        const uint16_t* const tB = buf + kTM * kStage;
+        u32x4_t af[2][4], bf[2][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            u32x4_t bf[2];
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) bf[nt] = fragment<kTN, BTR>(sB, 2 * wn + nt, s, lane);
+            for (int nt = 0; nt < 2; ++nt) bf[s][nt] = fragment<kTN, BTR>(tB, 2 * wn + nt, s, lane);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                const u32x4_t af = fragment<kTM, ATR>(sA, 4 * wm + mt, s, lane);
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af, bf[nt], acc[mt][nt]);
-            }
+            for (int mt = 0; mt < 4; ++mt) af[s][mt] = fragment<kTM, ATR>(tA, 4 * wm + mt, s, lane);
         }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[s][mt], bf[s][nt], acc[mt][nt]);
+    };
+    auto stage = [&](int64_t st, const uint16_t* cur, uint16_t* nxt) {
+        wait_moves<Mover<kTM, ATR>::N + Mover<kTN, BTR>::N>();
+        stage_barrier();
+        move(st + 2, nxt);
+        products(cur);
+    };
+    move(0, ring0);
+    move(1, ring1);
+    int64_t st = 0;
+    for (; st + 3 <= nst; st += 3) {
+        stage(st, ring0, ring2);
+        stage(st + 1, ring1, ring0);
+        stage(st + 2, ring2, ring1);
     }
-    __syncthreads();
+    if (st < nst) stage(st, ring0, ring2);
+    if (st + 1 < nst) stage(st + 1, ring1, ring0);
+    wait_moves<0>();
+    stage_barrier();
+}
+
+// Tile of this workgroup: ids go round-robin over the 8 XCDs, so each XCD is
+// dealt one run of neighbouring tiles, whose operands meet in its L2.
+__device__ __forceinline__ int64_t dealt_tile()
+{
+    const uint32_t nb = gridDim.x, b = blockIdx.x, per = nb / 8;
+    return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
 }
 
 // Logits of one 256-label x 128-row tile.  GRAD = false: the tile's (maximum,
@@ -212,15 +311,18 @@ __device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const
 template <int DT, bool GRAD>
 __global__ __launch_bounds__(256, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
+    HASTE_SM_RING
     __shared__ float red[2][kTN][2];
-    const int64_t mt0 = blockIdx.x / (a.Bp / kTN), n0 = blockIdx.x % (a.Bp / kTN) * kTN;
+    // eight label tiles by the row tiles in turn
+    const int64_t nrt = a.Bp / kTN, nlt = gridDim.x / nrt, t = dealt_tile();
+    const int64_t first = t / (8 * nrt) * 8, loc = t % (8 * nrt), gl = nlt - first < 8 ? nlt - first : 8;
+    const int64_t mt0 = first + loc % gl, n0 = loc / gl * kTN;
     const int nv = *a.nv;
     if (n0 >= nv) return;
     const int64_t m0 = l0 + mt0 * kTM;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
     f32x16_t acc[4][2];
-    tile_product<DT, false, false>(A, m0, B, n0, 0, a.Hp, sA, sB, acc);
+    tile_product<DT, false, false>(A, m0, B, n0, a.Hp / kStage, ring0, ring1, ring2, acc);
 
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
     const int hl = lane >> 5, r32 = lane & 31;
@@ -338,12 +440,12 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
 template <int DT>
 __global__ __launch_bounds__(256, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
-    const int64_t m0 = (int64_t)(blockIdx.x % ncols) * kTM, n0 = (int64_t)(blockIdx.x / ncols) * kTN;
+    HASTE_SM_RING
+    const int64_t t = dealt_tile(), m0 = t % ncols * kTM, n0 = t / ncols * kTN;
     const int nv = *a.nv;
     const Operand A{a.hc, a.Hp, a.Hp, a.Bp}, B{a.dz, a.Lc, a.Lc, a.Bp};
     f32x16_t acc[4][2];
-    tile_product<DT, true, true>(A, m0, B, n0, 0, (nv + kStage - 1) / kStage * kStage, sA, sB, acc);
+    tile_product<DT, true, true>(A, m0, B, n0, (nv + kStage - 1) / kStage, ring0, ring1, ring2, acc);
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
     const float f = a.scale / kDScale<DT>;
     uint16_t* dW = reinterpret_cast<uint16_t*>(a.dW);
@@ -369,17 +471,18 @@ __global__ __launch_bounds__(256, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int
 template <int DT>
 __global__ __launch_bounds__(256, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t sA[kTM * kStage], sB[kTN * kStage];
-    const int64_t nrows = a.Bp / kTN, s = blockIdx.x / (ncols * nrows), t = blockIdx.x % (ncols * nrows);
+    HASTE_SM_RING
+    const int64_t nrows = a.Bp / kTN, d = dealt_tile(), s = d / (ncols * nrows), t = d % (ncols * nrows);
     const int64_t m0 = (t % ncols) * kTM, n0 = t / ncols * kTN;
     if (n0 >= *a.nv) return;
     const int64_t len = (a.Lc / a.splits + kStage - 1) / kStage * kStage;
     const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;       // labels of the piece
     int64_t k0 = s * len, k1 = s == a.splits - 1 ? a.Lc : k0 + len;
     if (k1 > (live + kStage - 1) / kStage * kStage) k1 = (live + kStage - 1) / kStage * kStage;
-    const Operand A{reinterpret_cast<const uint16_t*>(a.W) + l0 * a.ldw, a.ldw, a.H, live}, B{a.dz, a.Lc, a.Bp, a.Lc};
+    const Operand A{reinterpret_cast<const uint16_t*>(a.W) + (l0 + k0) * a.ldw, a.ldw, a.H, live - k0};
+    const Operand B{a.dz + k0, a.Lc, a.Bp, a.Lc - k0};
     f32x16_t acc[4][2];
-    tile_product<DT, true, false>(A, m0, B, n0, k0, k1, sA, sB, acc);
+    tile_product<DT, true, false>(A, m0, B, n0, (k1 - k0) / kStage, ring0, ring1, ring2, acc);
     const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {

@@ -547,7 +547,7 @@ int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq,
  * summed in fp64.  D goes to the gradient products rounded to the operands'
  * type.  haste_softmax_loss computes loss, row_loss and lse alone.
  * All results are bitwise repeatable for one workspace size.
- * H % 8 == 0, H <= 16384, ldh and ldw multiples of 8, B <= 2^20,
+ * H % 8 == 0, H <= 16384, ldh and ldw multiples of 8 up to 2^22, B <= 2^20,
  * L <= 2^31 - 65; pointers 16-byte aligned.
  * Workspace: any size from haste_softmax_workspace_min (256 labels at a
  * time) up; haste_softmax_workspace_size gives the size past which more does
