@@ -47,22 +47,17 @@ int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_d
 // Softmax workspace: fixed parts, then the piece of D, whose length follows
 // from the bytes that are left.
 struct SoftmaxLayout {
-    int64_t Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
-    int splits;
+    int64_t tn, Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
     size_t nv, rows, rank, hit, clse, part, hc, dhp, dz;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
     {
-        Bp = round_up(B, kSmRowTile);
+        tn = sm_row_tile(B);
+        Bp = round_up(B, tn);
         Hp = round_up(H, 64);
         Lr = round_up(L, kSmLabelTile);
         const int64_t most = (256LL << 20) / (2 * Bp) / kSmLabelTile * kSmLabelTile;
         want = balanced(most < kSmLabelTile ? kSmLabelTile : most);
-        // two workgroups per CU for the feature gradient: label ranges of at
-        // least 128 labels whose partials are added afterwards
-        const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / kSmRowTile);
-        int64_t s = 512 / tiles;
-        if (s > want / 128) s = want / 128;
-        splits = (int)(s < 1 ? 1 : s);
+        const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / tn), slots = sm_dh_slots(tn);
         size_t at = 0;
         auto take = [&](size_t n) {
             const size_t o = at;
@@ -76,7 +71,7 @@ struct SoftmaxLayout {
         clse = take((size_t)Bp * 4);
         part = take((size_t)(Lr / kSmLabelTile) * (size_t)Bp * 8);
         hc = take((size_t)Bp * (size_t)Hp * 2);
-        dhp = grad ? take((size_t)splits * (size_t)Bp * (size_t)Hp * 4) : at;
+        dhp = grad ? take((size_t)(tiles > slots ? tiles : slots) * (size_t)(tn * kSmLabelTile) * 4) : at;
         dz = at;
     }
     int64_t balanced(int64_t most) const
@@ -92,7 +87,7 @@ int check_softmax_shape(int64_t B, int64_t H, int64_t L)
     if (B < 1 || H < 1 || L < 1) return HASTE_ERR_DIM;
     if (H % 8 != 0 || H > 16384 || B > (1 << 20) || L > kMaxLabels) return HASTE_ERR_UNSUPPORTED;
     // one workgroup per (label tile, row tile)
-    if (round_up(L, kSmLabelTile) / kSmLabelTile * (round_up(B, kSmRowTile) / kSmRowTile) >= (1LL << 31))
+    if (round_up(L, kSmLabelTile) / kSmLabelTile * ((B + 127) / 128) >= (1LL << 31))
         return HASTE_ERR_UNSUPPORTED;
     return HASTE_OK;
 }
@@ -118,7 +113,7 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.h = h; a.W = W; a.y_rowptr = y_rowptr; a.y_col = y_col;
     a.B = B; a.H = H; a.L = L; a.ldh = ldh; a.ldw = ldw; a.scale = scale;
     a.dW = dW; a.dh = dh; a.row_loss = row_loss; a.lse = lse; a.loss = loss;
-    a.Bp = l.Bp; a.Hp = l.Hp; a.splits = l.splits;
+    a.tn = l.tn; a.Bp = l.Bp; a.Hp = l.Hp; a.dh_slots = sm_dh_slots(l.tn);
     a.Lc = l.want;
     if (grad && workspace_bytes < l.total(l.want, true))
         a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / (2 * (size_t)l.Bp)) / kSmLabelTile * kSmLabelTile);

@@ -26,7 +26,6 @@ namespace haste {
 namespace {
 
 constexpr int kTM = (int)kSmLabelTile;   // 256
-constexpr int kTN = (int)kSmRowTile;     // 128
 constexpr int kStage = 32;               // contraction per LDS stage
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -48,6 +47,15 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c)
 // D is held times this in the workspace.
 template <int DT>
 constexpr float kDScale = DT == HASTE_F16 ? 4096.0f : 1.0f;
+
+// D lies in blocks of 256 labels, Bp rows of 512 bytes each, so that a tile
+// of it is one contiguous run (as one row per rank, the rows of a tile are
+// 64 KB and more apart; with the passes as they were, the blocks measured
+// 6 % on the whole step at 4096 x 131072).
+__device__ __forceinline__ int64_t dz_at(const SoftmaxArgs& a, int64_t rank, int64_t label)
+{
+    return (label / kTM * a.Bp + rank) * kTM + label % kTM;
+}
 
 // rows / rank / nv: the ranks of the rows that have labels, in row order.
 __global__ __launch_bounds__(1024) void k_sm_rows(const int32_t* __restrict__ rowptr, int64_t B, int64_t Bp,
@@ -126,14 +134,16 @@ struct Operand {
     int64_t ld;
     int64_t rows;     // valid tile-row indices: [0, rows), past it the last one is read again
     int64_t depth;    // valid contraction indices, likewise
+    int64_t block = 0;   // BLOCKED (TR = false): elements from one run of 256 contraction indices to the next
 };
 
-// s_waitcnt vmcnt(N) alone (expcnt and lgkmcnt at their no-wait maxima).
+// Waits until at most N of this wave's moves are in flight and its LDS reads
+// are done (vmcnt(N) and lgkmcnt(0), expcnt at its no-wait maximum).
 template <int N>
-__device__ __forceinline__ void wait_moves()
+__device__ __forceinline__ void wait_stage()
 {
     static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
 // Workgroup barrier without a memory fence (a fence would wait for every
 // move in flight); the empty asm statements keep the compiler from moving
@@ -153,12 +163,13 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // c (of T / 8) at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the pieces that
 // one operand read touches over the banks; since a lane's place in LDS is
 // fixed, the swizzle is in the piece it asks for.
-template <int T, bool TR>
+template <int T, bool TR, int THREADS, bool BLOCKED = false>
 struct Mover {
-    static constexpr int N = T / 64;          // moves per wave and stage
+    static_assert(!(TR && BLOCKED), "");
+    static constexpr int N = 4 * T / THREADS;   // moves per wave and stage
     const char* base;                         // tile's first row (TR: column), contraction index 0
     uint32_t off[N];                          // byte offset of the lane's piece
-    int64_t step;                             // TR: bytes per stage
+    int64_t step;                             // TR: bytes per stage; BLOCKED: bytes per block
     uint32_t row[N], pitch;                   // contraction index within the stage, bytes per row
     int64_t depth;
 
@@ -171,7 +182,7 @@ struct Mover {
             step = 2 * kStage * o.ld;
         } else {
             base = reinterpret_cast<const char*>(o.p + r0 * o.ld);
-            step = 0;
+            step = 2 * o.block;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -192,16 +203,20 @@ struct Mover {
     }
 
     // stage st into buf; pieces past the operand's depth repeat its last one
-    __device__ __forceinline__ void move(int64_t st, uint16_t* buf, int wave) const
+    __device__ __forceinline__ void move(int st, uint16_t* buf, int wave) const
     {
-        const char* const b = TR ? base + st * step : base;
+        const char* b = base;
+        if constexpr (TR) b += (int64_t)st * step;
+        if constexpr (BLOCKED) b += (int64_t)(st / (256 / kStage)) * step + 2 * kStage * (st % (256 / kStage));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             uint32_t o;
             if constexpr (TR) {
-                const int64_t left = depth - st * kStage;
+                const int left = (int)depth - st * kStage;
                 const uint32_t last = left < kStage ? (uint32_t)left - 1 : kStage - 1;
                 o = off[i] + (row[i] < last ? row[i] : last) * pitch;
+            } else if constexpr (BLOCKED) {
+                o = off[i] + 2 * row[i];
             } else {
                 const uint32_t k = (uint32_t)st * kStage + row[i], last = (uint32_t)depth - 8;
                 o = off[i] + 2 * (k < last ? k : last);
@@ -211,89 +226,154 @@ struct Mover {
     }
 };
 
-// Operand fragment of the 32 tile rows 32 x .., contraction step s (16 deep).
-template <int T, bool TR>
-__device__ __forceinline__ u32x4_t fragment(const uint16_t* tile, int x, int s, int lane)
+// LDS byte address of a pointer into LDS.
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p)
 {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t*)p;
+}
+
+// Operand fragments of NF x 32 tile rows from row 32 x0 on, contraction step s
+// (16 deep).
+//
+// TR operands are read with the transposing LDS read in groups, each group
+// and its wait in one asm block: through the builtin, the compiler (which
+// does not see that the read and the moves in flight touch different
+// buffers) waits for every move first, and the ring is empty at each stage.
+template <int T, bool TR, int NF>
+__device__ __forceinline__ void fragments(const uint16_t* tile, int x0, int s, int lane, u32x4_t (&f)[NF])
+{
+    static_assert(NF == 2 || NF == 4, "");
     if constexpr (TR) {
+        // lane 16 g + 4 rr + cc: contraction row 16 s + 8 (g / 2) + rr (and + 4), piece 4 x + 2 (g % 2) + cc / 2
         const int g = lane >> 4, rr = (lane >> 2) & 3, cc = lane & 3;
-        const int piece = 4 * x + 2 * (g & 1) + (cc >> 1);
-        const uint16_t* p = tile + (16 * s + 8 * (g >> 1) + rr) * T + 8 * (piece ^ (4 * rr)) + 4 * (cc & 1);
-        return cat(lds_tr16(p), lds_tr16(p + 4 * T));
+        const uint32_t base = lds_address(tile + (16 * s + 8 * (g >> 1) + rr) * T + 8 * (2 * (g & 1) + (cc >> 1)) + 4 * (cc & 1));
+        uint32_t p[NF];
+#pragma unroll
+        for (int i = 0; i < NF; ++i) p[i] = base + 64 * (uint32_t)((x0 + i) ^ rr);
+        u32x2_t v[2 * NF];
+        if constexpr (NF == 4)
+            asm volatile("ds_read_b64_tr_b16 %0, %8\n\t"
+                         "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %2, %9\n\t"
+                         "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %4, %10\n\t"
+                         "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+                         "ds_read_b64_tr_b16 %6, %11\n\t"
+                         "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]),
+                           "=&v"(v[7])
+                         : "v"(p[0]), "v"(p[1]), "v"(p[2]), "v"(p[3]), "n"(8 * T)
+                         : "memory");
+        else
+            asm volatile("ds_read_b64_tr_b16 %0, %4\n\t"
+                         "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+                         "ds_read_b64_tr_b16 %2, %5\n\t"
+                         "ds_read_b64_tr_b16 %3, %5 offset:%6\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+                         : "v"(p[0]), "v"(p[1]), "n"(8 * T)
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < NF; ++i) f[i] = cat(v[2 * i], v[2 * i + 1]);
     } else {
-        const int r = 32 * x + (lane & 31);
-        return *reinterpret_cast<const u32x4_t*>(tile + r * kStage + 8 * ((2 * s + (lane >> 5)) ^ ((r >> 2) & 3)));
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+            const int r = 32 * (x0 + i) + (lane & 31);
+            f[i] = *reinterpret_cast<const u32x4_t*>(tile + r * kStage + 8 * ((2 * s + (lane >> 5)) ^ ((r >> 2) & 3)));
+        }
     }
 }
 
-// The stage ring: three buffers of both operands' tiles (72 KB: two
-// workgroups per CU).  Distinct objects, so that the compiler sees that an
-// operand read and a move in flight never meet and adds no waits.
-constexpr int kRing = (kTM + kTN) * kStage;
-#define HASTE_SM_RING                                              \
-    __shared__ __attribute__((aligned(1024))) uint16_t ring0[kRing]; \
-    __shared__ __attribute__((aligned(1024))) uint16_t ring1[kRing]; \
-    __shared__ __attribute__((aligned(1024))) uint16_t ring2[kRing];
+// Tile shapes: 256 x TN, TN = 256 by eight waves or TN = 128 by four; each
+// wave owns 128 x 64 of it (wave w: tile rows 128 (w % 2) .., columns
+// 64 (w / 2) ..).  The wide tile asks L2 for a third fewer operand bytes per
+// product, which is what bounds large products here; the narrow one serves
+// batches of up to 128 rows.
+template <int TN>
+constexpr int kThreads = 2 * TN;
+// The stage ring: R buffers of both operands' tiles, 128 KB of LDS for the
+// wide tile (one workgroup per CU), 72 KB for the narrow one (two).  Distinct
+// objects, so that the compiler sees that an operand read and a move in
+// flight never meet and adds no waits.
+template <int TN>
+constexpr int kRing = TN == 256 ? 4 : 3;
+template <int TN>
+constexpr int kBuf = (kTM + TN) * kStage;
+#define HASTE_SM_RING(TN)                                                                    \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring0[kBuf<TN>], ring1[kBuf<TN>];     \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring2[kBuf<TN>];                      \
+    __shared__ __attribute__((aligned(1024))) uint16_t ring3[kRing<TN> == 4 ? kBuf<TN> : 8]; \
+    uint16_t* const ring[4] = {ring0, ring1, ring2, ring3};
 
-// acc (4 x 2 tiles of 32 x 32 per wave; wave w: tile rows 128 (w / 2) ..,
-// columns 64 (w % 2) ..) += A B^T over nst stages of 32.  Per stage: wait for
-// this wave's moves of the stage (the next stage's stay in flight), one
-// barrier (everyone's moves are done, and the buffer read one stage ago is
-// free), the moves of the stage two ahead, the products.  On return no move
-// is in flight and the ring is free.
-template <int DT, bool ATR, bool BTR>
-__device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int64_t nst,
-                                             uint16_t* ring0, uint16_t* ring1, uint16_t* ring2, f32x16_t (&acc)[4][2])
+// acc (4 x 2 tiles of 32 x 32 per wave) = A B^T over nst stages of 32.  A
+// stage's second half of operands is read while the products of its first
+// half run; then, once this wave's moves of the next stage are done, one
+// barrier: everyone's are, and everyone has read this stage.  After it the
+// stage's buffer takes the moves of the stage R ahead, and the next stage's
+// first half is read under the second half's products.  On return no move is
+// in flight and the ring is free.
+template <int DT, int TN, bool ATR, bool BTR, bool BBLOCKED = false>
+__device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int nst,
+                                             uint16_t* const (&ring)[4], f32x16_t (&acc)[4][2])
 {
+    constexpr int R = kRing<TN>;
     const int tid = threadIdx.x, lane = tid & 63;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w & 1, wn = w >> 1;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = f32x16_t{};
     if (nst <= 0) return;
-    const Mover<kTM, ATR> ma(A, m0, w, lane);
-    const Mover<kTN, BTR> mb(B, n0, w, lane);
-    auto move = [&](int64_t st, uint16_t* buf) {
-        const int64_t s = st < nst ? st : nst - 1;       // past the end: into a buffer nobody reads
+    using MA = Mover<kTM, ATR, kThreads<TN>>;
+    using MB = Mover<TN, BTR, kThreads<TN>, BBLOCKED>;
+    const MA ma(A, m0, w, lane);
+    const MB mb(B, n0, w, lane);
+    auto move = [&](int st, uint16_t* buf) {
+        const int s = st < nst ? st : nst - 1;       // past the end: into a buffer nobody reads
         ma.move(s, buf, w);
         mb.move(s, buf + kTM * kStage, w);
     };
-    auto products = [&](const uint16_t* buf) {
-        const uint16_t* const tA = buf;
-        const uint16_t* const tB = buf + kTM * kStage;
-        u32x4_t af[2][4], bf[2][2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) bf[s][nt] = fragment<kTN, BTR>(tB, 2 * wn + nt, s, lane);
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) af[s][mt] = fragment<kTM, ATR>(tA, 4 * wm + mt, s, lane);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[s][mt], bf[s][nt], acc[mt][nt]);
+    u32x4_t af[2][4], bf[2][2];
+    auto read = [&](const uint16_t* buf, int s) {
+        fragments<TN, BTR>(buf + kTM * kStage, 2 * wn, s, lane, bf[s]);
+        fragments<kTM, ATR>(buf, 4 * wm, s, lane, af[s]);
     };
-    auto stage = [&](int64_t st, const uint16_t* cur, uint16_t* nxt) {
-        wait_moves<Mover<kTM, ATR>::N + Mover<kTN, BTR>::N>();
+    auto products = [&](int s) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[s][mt], bf[s][nt], acc[mt][nt]);
+    };
+    // (the scheduling barriers hold the reads ahead of the products: left
+    // alone, the compiler puts each read right before its use)
+    auto stage = [&](int st, uint16_t* cur, const uint16_t* next) {
+        read(cur, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        products(0);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_stage<(R - 2) * (MA::N + MB::N)>();
         stage_barrier();
-        move(st + 2, nxt);
-        products(cur);
+        move(st + R, cur);
+        read(next, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        products(1);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    move(0, ring0);
-    move(1, ring1);
-    int64_t st = 0;
-    for (; st + 3 <= nst; st += 3) {
-        stage(st, ring0, ring2);
-        stage(st + 1, ring1, ring0);
-        stage(st + 2, ring2, ring1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) move(r, ring[r]);
+    wait_stage<(R - 1) * (MA::N + MB::N)>();
+    stage_barrier();
+    read(ring[0], 0);
+    int st = 0;
+    for (; st + R <= nst; st += R) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) stage(st + r, ring[r], ring[(r + 1) % R]);
     }
-    if (st < nst) stage(st, ring0, ring2);
-    if (st + 1 < nst) stage(st + 1, ring1, ring0);
-    wait_moves<0>();
+    if (st < nst) stage(st, ring[0], ring[1]);
+    if (st + 1 < nst) stage(st + 1, ring[1], ring[2]);
+    if (R == 4 && st + 2 < nst) stage(st + 2, ring[2], ring[3]);
+    wait_stage<0>();
     stage_barrier();
 }
 
@@ -305,26 +385,26 @@ __device__ __forceinline__ int64_t dealt_tile()
     return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
 }
 
-// Logits of one 256-label x 128-row tile.  GRAD = false: the tile's (maximum,
+// Logits of one 256-label x TN-row tile.  GRAD = false: the tile's (maximum,
 // sum of exponentials) per row.  GRAD = true: D = exp(z - lse) of the piece
 // of labels [l0, l0 + Lc), without the labels' own terms.
-template <int DT, bool GRAD>
-__global__ __launch_bounds__(256, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
+template <int DT, int TN, bool GRAD>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
 {
-    HASTE_SM_RING
-    __shared__ float red[2][kTN][2];
+    HASTE_SM_RING(TN)
+    __shared__ float red[2][TN][2];
     // eight label tiles by the row tiles in turn
-    const int64_t nrt = a.Bp / kTN, nlt = gridDim.x / nrt, t = dealt_tile();
+    const int64_t nrt = a.Bp / TN, nlt = gridDim.x / nrt, t = dealt_tile();
     const int64_t first = t / (8 * nrt) * 8, loc = t % (8 * nrt), gl = nlt - first < 8 ? nlt - first : 8;
-    const int64_t mt0 = first + loc % gl, n0 = loc / gl * kTN;
+    const int64_t mt0 = first + loc % gl, n0 = loc / gl * TN;
     const int nv = *a.nv;
     if (n0 >= nv) return;
     const int64_t m0 = l0 + mt0 * kTM;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
     f32x16_t acc[4][2];
-    tile_product<DT, false, false>(A, m0, B, n0, a.Hp / kStage, ring0, ring1, ring2, acc);
+    tile_product<DT, TN, false, false>(A, m0, B, n0, (int)(a.Hp / kStage), ring, acc);
 
-    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const int hl = lane >> 5, r32 = lane & 31;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
@@ -362,14 +442,14 @@ __global__ __launch_bounds__(256, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
                     for (int i = 0; i < 4; ++i)
                         d[i] = l0 + m + i < a.L ? __builtin_amdgcn_exp2f((acc[mt][nt][4 * g + i] - lse) * kLog2e) * f
                                                 : 0.f;
-                    *reinterpret_cast<u32x2_t*>(a.dz + n * a.Lc + m) =
+                    *reinterpret_cast<u32x2_t*>(a.dz + dz_at(a, n, m)) =
                         u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
                 }
         }
     }
     if constexpr (!GRAD) {
         __syncthreads();
-        if (threadIdx.x < kTN) {
+        if (threadIdx.x < TN) {
             const float t0 = red[0][threadIdx.x][0], t1 = red[1][threadIdx.x][0];
             const float top = fmaxf(t0, t1), base = top == -INFINITY ? 0.f : top;
             const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f((t0 - base) * kLog2e) +
@@ -432,21 +512,22 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
         const float d = (__builtin_amdgcn_exp2f((z - lse) * kLog2e) - share) * kDScale<DT>;
-        if (lane == 0) a.dz[i * a.Lc + (l - l0)] = (uint16_t)pack2<DT>(d, 0.f);
+        if (lane == 0) a.dz[dz_at(a, i, l - l0)] = (uint16_t)pack2<DT>(d, 0.f);
     }
 }
 
-// dW of one tile of 256 columns x 128 labels of the piece.
-template <int DT>
-__global__ __launch_bounds__(256, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
+// dW of one tile of 256 columns x TN labels of the piece.
+template <int DT, int TN>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
 {
-    HASTE_SM_RING
-    const int64_t t = dealt_tile(), m0 = t % ncols * kTM, n0 = t / ncols * kTN;
+    HASTE_SM_RING(TN)
+    const int64_t t = dealt_tile(), m0 = t % ncols * kTM, n0 = t / ncols * TN;
     const int nv = *a.nv;
-    const Operand A{a.hc, a.Hp, a.Hp, a.Bp}, B{a.dz, a.Lc, a.Lc, a.Bp};
+    const Operand A{a.hc, a.Hp, a.Hp, a.Bp};
+    const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
     f32x16_t acc[4][2];
-    tile_product<DT, true, true>(A, m0, B, n0, (nv + kStage - 1) / kStage, ring0, ring1, ring2, acc);
-    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+    tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage - 1) / kStage, ring, acc);
+    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const float f = a.scale / kDScale<DT>;
     uint16_t* dW = reinterpret_cast<uint16_t*>(a.dW);
 #pragma unroll
@@ -465,25 +546,36 @@ __global__ __launch_bounds__(256, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int
     }
 }
 
-// The piece's share of dh: 256 columns x 128 ranks over one of `splits`
-// ranges of its labels, added to (or, for the first piece, stored in) that
-// range's partial.
-template <int DT>
-__global__ __launch_bounds__(256, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
+// Label ranges that the feature gradient of nv rows is split into: as many
+// as fill the grid once, in whole blocks of D.
+__device__ __forceinline__ int64_t dh_splits(const SoftmaxArgs& a, int64_t tiles)
 {
-    HASTE_SM_RING
-    const int64_t nrows = a.Bp / kTN, d = dealt_tile(), s = d / (ncols * nrows), t = d % (ncols * nrows);
-    const int64_t m0 = (t % ncols) * kTM, n0 = t / ncols * kTN;
-    if (n0 >= *a.nv) return;
-    const int64_t len = (a.Lc / a.splits + kStage - 1) / kStage * kStage;
+    int64_t s = a.dh_slots / tiles;
+    if (s > a.Lc / kTM) s = a.Lc / kTM;
+    return s < 1 ? 1 : s;
+}
+
+// The piece's share of dh: 256 columns x TN ranks over one range of its
+// labels, added to (or, for the first piece, stored in) that range's partial
+// (ranges x live rows, in whole tiles, x Hp).
+template <int DT, int TN>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
+{
+    HASTE_SM_RING(TN)
+    const int64_t nvt = (*a.nv + TN - 1) / TN, tiles = ncols * nvt;
+    if (tiles == 0) return;
+    const int64_t splits = dh_splits(a, tiles), d = dealt_tile(), s = d / tiles, t = d % tiles;
+    if (s >= splits) return;
+    const int64_t m0 = t % ncols * kTM, n0 = t / ncols * TN;
+    const int64_t len = (a.Lc / splits + kTM - 1) / kTM * kTM;
     const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;       // labels of the piece
-    int64_t k0 = s * len, k1 = s == a.splits - 1 ? a.Lc : k0 + len;
+    int64_t k0 = s * len, k1 = s == splits - 1 ? a.Lc : k0 + len;
     if (k1 > (live + kStage - 1) / kStage * kStage) k1 = (live + kStage - 1) / kStage * kStage;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W) + (l0 + k0) * a.ldw, a.ldw, a.H, live - k0};
-    const Operand B{a.dz + k0, a.Lc, a.Bp, a.Lc - k0};
+    const Operand B{a.dz + dz_at(a, 0, k0), kTM, a.Bp, a.Lc - k0, a.Bp * kTM};
     f32x16_t acc[4][2];
-    tile_product<DT, true, false>(A, m0, B, n0, (k1 - k0) / kStage, ring0, ring1, ring2, acc);
-    const int lane = threadIdx.x & 63, wm = threadIdx.x >> 7, wn = (threadIdx.x >> 6) & 1;
+    tile_product<DT, TN, true, false, true>(A, m0, B, n0, (int)((k1 - k0) / kStage), ring, acc);
+    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
         const int64_t n = n0 + 64 * wn + 32 * nt + (lane & 31);
@@ -493,7 +585,7 @@ __global__ __launch_bounds__(256, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int
             for (int g = 0; g < 4; ++g) {
                 const int64_t j = m0 + 128 * wm + 32 * mt + 8 * g + 4 * (lane >> 5);
                 if (j >= a.Hp) continue;
-                f32x4_t* o = reinterpret_cast<f32x4_t*>(a.dhp + (s * a.Bp + n) * a.Hp + j);
+                f32x4_t* o = reinterpret_cast<f32x4_t*>(a.dhp + (s * nvt * TN + n) * a.Hp + j);
                 f32x4_t v = {acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2], acc[mt][nt][4 * g + 3]};
                 if (!first) v += *o;
                 *o = v;
@@ -504,7 +596,7 @@ __global__ __launch_bounds__(256, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int
 // dh by row from the partials (0 for rows without labels); workgroup 0 also
 // adds up the loss, in 64 bits and a fixed order.
 template <int DT>
-__global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad)
+__global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int64_t ncols)
 {
     if (blockIdx.x == 0) {
         __shared__ double sh[256];
@@ -522,15 +614,18 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad)
     if (!grad) return;
     const int64_t per = a.H / 8, n = a.B * per;
     const float f = a.scale / kDScale<DT>;
+    const int64_t nvt = (*a.nv + a.tn - 1) / a.tn;
+    const int64_t splits = nvt ? dh_splits(a, ncols * nvt) : 0;
     for (int64_t t = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; t < n; t += (int64_t)(gridDim.x - 1) * 256) {
         const int64_t b = t / per, j = 8 * (t % per), i = a.rank[b];
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 0.f;
         if (i >= 0) {
-            for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+            for (int64_t s = 0; s < splits; ++s) {
                 float w[8];
-                widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * a.Bp + i) * a.Hp + j, 8), w);
+                widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * a.tn + i) * a.Hp + j, 8), w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] += w[e];
             }
@@ -541,26 +636,35 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad)
     }
 }
 
-template <int DT>
+template <int DT, int TN>
 void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
 {
-    const int64_t nrt = a.Bp / kTN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
+    constexpr int NT = kThreads<TN>;
+    const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
     k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
     k_sm_gather<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a);
-    k_sm_logits<DT, false><<<(unsigned)(tiles * nrt), 256, 0, s>>>(a, 0);
+    k_sm_logits<DT, TN, false><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0);
     k_sm_lse<<<(unsigned)((a.Bp + 15) / 16), 256, 0, s>>>(a, tiles);
     if (grad) {
+        const int64_t dh_grid = ncols * nrt > a.dh_slots ? ncols * nrt : a.dh_slots;
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
-            k_sm_logits<DT, true><<<(unsigned)(lt * nrt), 256, 0, s>>>(a, l0);
+            k_sm_logits<DT, TN, true><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0);
             k_sm_labels<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a, l0);
-            k_sm_dw<DT><<<(unsigned)((live + kTN - 1) / kTN * ncols), 256, 0, s>>>(a, l0, ncols);
-            k_sm_dh<DT><<<(unsigned)(ncols * nrt * a.splits), 256, 0, s>>>(a, l0, ncols, l0 == 0);
+            k_sm_dw<DT, TN><<<(unsigned)((live + TN - 1) / TN * ncols), NT, 0, s>>>(a, l0, ncols);
+            k_sm_dh<DT, TN><<<(unsigned)dh_grid, NT, 0, s>>>(a, l0, ncols, l0 == 0);
         }
     }
     const int64_t blocks = grad ? (a.B * (a.H / 8) + 255) / 256 : 0;
-    k_sm_finish<DT><<<(unsigned)(1 + (blocks > 4096 ? 4096 : blocks)), 256, 0, s>>>(a, grad);
+    k_sm_finish<DT><<<(unsigned)(1 + (blocks > 4096 ? 4096 : blocks)), 256, 0, s>>>(a, grad, ncols);
+}
+
+template <int DT>
+void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
+{
+    if (a.tn == 256) run<DT, 256>(grad, a, s);
+    else run<DT, 128>(grad, a, s);
 }
 
 }  // namespace

@@ -263,9 +263,10 @@ struct SoftmaxArgs {
     float* lse;             // B
     float* loss;            // 1
     // workspace
-    int64_t Bp, Hp;         // B and H rounded up to kSmRowTile and 64
+    int64_t tn;             // rows per tile: sm_row_tile(B)
+    int64_t Bp, Hp;         // B and H rounded up to tn and 64
     int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
-    int splits;             // label ranges of a piece's feature gradient
+    int64_t dh_slots;       // workgroups that fill the chip with feature-gradient tiles
     int32_t* nv;
     int32_t* rows;          // Bp
     int32_t* rank;          // B, -1 for rows without labels
@@ -273,10 +274,13 @@ struct SoftmaxArgs {
     float* clse;            // Bp: log-sum-exp by rank
     float* part;            // label tiles x Bp x (max, sum)
     uint16_t* hc;           // Bp x Hp
-    uint16_t* dz;           // Bp x Lc
-    float* dhp;             // splits x Bp x Hp
+    uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
+    float* dhp;             // partials of dh, at most max(dh_slots, tiles) tiles of 256 x tn
 };
-constexpr int64_t kSmLabelTile = 256, kSmRowTile = 128;
+constexpr int64_t kSmLabelTile = 256;
+constexpr int64_t sm_row_tile(int64_t B) { return B > 128 ? 256 : 128; }
+// one workgroup of the wide tile per CU, two of the narrow one
+constexpr int64_t sm_dh_slots(int64_t tn) { return tn == 256 ? 256 : 512; }
 void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s);
 
 }  // namespace haste
