@@ -26,7 +26,9 @@ namespace haste {
 namespace {
 
 constexpr int kTM = (int)kSmLabelTile;   // 256
-constexpr int kStage = 32;               // contraction per LDS stage
+// Contraction per LDS stage of a tile TN wide.
+template <int TN>
+constexpr int kStage = TN == 256 ? 64 : 32;
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
@@ -47,6 +49,8 @@ __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c)
 // D is held times this in the workspace.
 template <int DT>
 constexpr float kDScale = DT == HASTE_F16 ? 4096.0f : 1.0f;
+template <int DT>
+constexpr float kDLog2 = DT == HASTE_F16 ? 12.0f : 0.0f;
 
 // D lies in blocks of 256 labels, Bp rows of 512 bytes each, so that a tile
 // of it is one contiguous run (as one row per rank, the rows of a tile are
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
     if (threadIdx.x == 0) a.hit[i] = ((sh[0] + sh[1]) + (sh[2] + sh[3])) / (float)(p1 - p0);
 }
 
-// An operand tile: T (256 or 128) tile rows by 32 contraction elements.
+// An operand tile: T (256 or 128) tile rows by one stage of ST contraction elements.
 // Contraction-contiguous operands (TR = false) lie in memory as one row of
 // `ld` elements per tile row; row-contiguous ones (TR = true) as one row of
 // ld elements per contraction index, with the tile rows along it.
@@ -159,14 +163,20 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // Moves of one operand tile from memory straight into LDS
 // (global_load_lds_dwordx4: a lane's 16 bytes land at the wave's LDS base +
 // 16 x lane).  LDS images in 16-byte pieces: TR = false: tile row r, piece
-// c (of 4) at 4 r + (c ^ (r / 4) % 4).  TR = true: contraction row k, piece
-// c (of T / 8) at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the pieces that
-// one operand read touches over the banks; since a lane's place in LDS is
-// fixed, the swizzle is in the piece it asks for.
-template <int T, bool TR, int THREADS, bool BLOCKED = false>
+// c (of P = ST / 8) at P r + (c ^ row_swizzle(r)).  TR = true: contraction
+// row k, piece c (of T / 8) at (T / 8) k + (c ^ 4 (k % 4)).  Both spread the
+// pieces that one operand read touches over the banks; since a lane's place
+// in LDS is fixed, the swizzle is in the piece it asks for.
+template <int ST>
+__device__ __forceinline__ int row_swizzle(int r)
+{
+    return ST == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+
+template <int T, bool TR, int ST, int THREADS, bool BLOCKED = false>
 struct Mover {
     static_assert(!(TR && BLOCKED), "");
-    static constexpr int N = 4 * T / THREADS;   // moves per wave and stage
+    static constexpr int N = T * ST / 8 / THREADS;   // moves per wave and stage
     const char* base;                         // tile's first row (TR: column), contraction index 0
     uint32_t off[N];                          // byte offset of the lane's piece
     int64_t step;                             // TR: bytes per stage; BLOCKED: bytes per block
@@ -179,7 +189,7 @@ struct Mover {
         pitch = 2 * (uint32_t)o.ld;
         if constexpr (TR) {
             base = reinterpret_cast<const char*>(o.p);
-            step = 2 * kStage * o.ld;
+            step = 2 * ST * o.ld;
         } else {
             base = reinterpret_cast<const char*>(o.p + r0 * o.ld);
             step = 2 * o.block;
@@ -194,7 +204,7 @@ struct Mover {
                 row[i] = (uint32_t)k;
                 off[i] = 2 * (uint32_t)r;
             } else {
-                const int r = u / 4, c = (u % 4) ^ ((r >> 2) & 3);
+                const int r = u / (ST / 8), c = (u % (ST / 8)) ^ row_swizzle<ST>(r);
                 const int64_t last = o.rows - 1 - r0;
                 row[i] = 8 * (uint32_t)c;
                 off[i] = (uint32_t)(r < last ? r : last) * pitch;
@@ -207,18 +217,18 @@ struct Mover {
     {
         const char* b = base;
         if constexpr (TR) b += (int64_t)st * step;
-        if constexpr (BLOCKED) b += (int64_t)(st / (256 / kStage)) * step + 2 * kStage * (st % (256 / kStage));
+        if constexpr (BLOCKED) b += (int64_t)(st / (256 / ST)) * step + 2 * ST * (st % (256 / ST));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             uint32_t o;
             if constexpr (TR) {
-                const int left = (int)depth - st * kStage;
-                const uint32_t last = left < kStage ? (uint32_t)left - 1 : kStage - 1;
+                const int left = (int)depth - st * ST;
+                const uint32_t last = left < ST ? (uint32_t)left - 1 : ST - 1;
                 o = off[i] + (row[i] < last ? row[i] : last) * pitch;
             } else if constexpr (BLOCKED) {
                 o = off[i] + 2 * row[i];
             } else {
-                const uint32_t k = (uint32_t)st * kStage + row[i], last = (uint32_t)depth - 8;
+                const uint32_t k = (uint32_t)st * ST + row[i], last = (uint32_t)depth - 8;
                 o = off[i] + 2 * (k < last ? k : last);
             }
             __builtin_amdgcn_global_load_lds(b + o, (lds_ptr)(buf + 512 * (N * wave + i)), 16, 0, 0);
@@ -239,7 +249,7 @@ __device__ __forceinline__ uint32_t lds_address(const uint16_t* p)
 // and its wait in one asm block: through the builtin, the compiler (which
 // does not see that the read and the moves in flight touch different
 // buffers) waits for every move first, and the ring is empty at each stage.
-template <int T, bool TR, int NF>
+template <int T, bool TR, int ST, int NF>
 __device__ __forceinline__ void fragments(const uint16_t* tile, int x0, int s, int lane, u32x4_t (&f)[NF])
 {
     static_assert(NF == 2 || NF == 4, "");
@@ -280,7 +290,7 @@ __device__ __forceinline__ void fragments(const uint16_t* tile, int x0, int s, i
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
             const int r = 32 * (x0 + i) + (lane & 31);
-            f[i] = *reinterpret_cast<const u32x4_t*>(tile + r * kStage + 8 * ((2 * s + (lane >> 5)) ^ ((r >> 2) & 3)));
+            f[i] = *reinterpret_cast<const u32x4_t*>(tile + r * ST + 8 * ((2 * s + (lane >> 5)) ^ row_swizzle<ST>(r)));
         }
     }
 }
@@ -292,32 +302,32 @@ __device__ __forceinline__ void fragments(const uint16_t* tile, int x0, int s, i
 // batches of up to 128 rows.
 template <int TN>
 constexpr int kThreads = 2 * TN;
-// The stage ring: R buffers of both operands' tiles, 128 KB of LDS for the
-// wide tile (one workgroup per CU), 72 KB for the narrow one (two).  Distinct
-// objects, so that the compiler sees that an operand read and a move in
-// flight never meet and adds no waits.
+// The stage ring: R buffers of both operands' tiles.  The wide tile takes two
+// stages of 64 (128 KB of LDS, one workgroup per CU): its moves then ask for
+// whole 128-byte lines, and with stages of 32 the half lines cost a third of
+// the logits passes.  The narrow one takes three stages of 32 (72 KB, two
+// workgroups per CU).  Distinct objects, so that the compiler sees that an
+// operand read and a move in flight never meet and adds no waits.
 template <int TN>
-constexpr int kRing = TN == 256 ? 4 : 3;
+constexpr int kRing = TN == 256 ? 2 : 3;
 template <int TN>
-constexpr int kBuf = (kTM + TN) * kStage;
+constexpr int kBuf = (kTM + TN) * kStage<TN>;
 #define HASTE_SM_RING(TN)                                                                    \
     __shared__ __attribute__((aligned(1024))) uint16_t ring0[kBuf<TN>], ring1[kBuf<TN>];     \
-    __shared__ __attribute__((aligned(1024))) uint16_t ring2[kBuf<TN>];                      \
-    __shared__ __attribute__((aligned(1024))) uint16_t ring3[kRing<TN> == 4 ? kBuf<TN> : 8]; \
-    uint16_t* const ring[4] = {ring0, ring1, ring2, ring3};
+    __shared__ __attribute__((aligned(1024))) uint16_t ring2[kRing<TN> == 3 ? kBuf<TN> : 8]; \
+    uint16_t* const ring[3] = {ring0, ring1, ring2};
 
-// acc (4 x 2 tiles of 32 x 32 per wave) = A B^T over nst stages of 32.  A
-// stage's second half of operands is read while the products of its first
-// half run; then, once this wave's moves of the next stage are done, one
-// barrier: everyone's are, and everyone has read this stage.  After it the
-// stage's buffer takes the moves of the stage R ahead, and the next stage's
-// first half is read under the second half's products.  On return no move is
-// in flight and the ring is free.
+// acc (4 x 2 tiles of 32 x 32 per wave) = A B^T over nst stages.  Each 16-deep
+// step's operands are read while the products of the step before run.  Ahead
+// of a stage's last products, once this wave's moves of the next stage are
+// done, one barrier: everyone's are, and everyone has read this stage.  After
+// it the stage's buffer takes the moves of the stage R ahead.  On return no
+// move is in flight and the ring is free.
 template <int DT, int TN, bool ATR, bool BTR, bool BBLOCKED = false>
 __device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const Operand& B, int64_t n0, int nst,
-                                             uint16_t* const (&ring)[4], f32x16_t (&acc)[4][2])
+                                             uint16_t* const (&ring)[3], f32x16_t (&acc)[4][2])
 {
-    constexpr int R = kRing<TN>;
+    constexpr int R = kRing<TN>, ST = kStage<TN>, S = ST / 16;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w & 1, wn = w >> 1;
 #pragma unroll
@@ -325,39 +335,42 @@ __device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = f32x16_t{};
     if (nst <= 0) return;
-    using MA = Mover<kTM, ATR, kThreads<TN>>;
-    using MB = Mover<TN, BTR, kThreads<TN>, BBLOCKED>;
+    using MA = Mover<kTM, ATR, ST, kThreads<TN>>;
+    using MB = Mover<TN, BTR, ST, kThreads<TN>, BBLOCKED>;
     const MA ma(A, m0, w, lane);
     const MB mb(B, n0, w, lane);
     auto move = [&](int st, uint16_t* buf) {
         const int s = st < nst ? st : nst - 1;       // past the end: into a buffer nobody reads
         ma.move(s, buf, w);
-        mb.move(s, buf + kTM * kStage, w);
+        mb.move(s, buf + kTM * ST, w);
     };
     u32x4_t af[2][4], bf[2][2];
     auto read = [&](const uint16_t* buf, int s) {
-        fragments<TN, BTR>(buf + kTM * kStage, 2 * wn, s, lane, bf[s]);
-        fragments<kTM, ATR>(buf, 4 * wm, s, lane, af[s]);
+        fragments<TN, BTR, ST>(buf + kTM * ST, 2 * wn, s, lane, bf[s & 1]);
+        fragments<kTM, ATR, ST>(buf, 4 * wm, s, lane, af[s & 1]);
     };
     auto products = [&](int s) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[s][mt], bf[s][nt], acc[mt][nt]);
+            for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[s & 1][mt], bf[s & 1][nt], acc[mt][nt]);
     };
     // (the scheduling barriers hold the reads ahead of the products: left
     // alone, the compiler puts each read right before its use)
     auto stage = [&](int st, uint16_t* cur, const uint16_t* next) {
-        read(cur, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        products(0);
-        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) {
+            read(cur, s + 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products(s);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         wait_stage<(R - 2) * (MA::N + MB::N)>();
         stage_barrier();
         move(st + R, cur);
         read(next, 0);
         __builtin_amdgcn_sched_barrier(0);
-        products(1);
+        products(S - 1);
         __builtin_amdgcn_sched_barrier(0);
     };
 #pragma unroll
@@ -371,8 +384,7 @@ __device__ __forceinline__ void tile_product(const Operand& A, int64_t m0, const
         for (int r = 0; r < R; ++r) stage(st + r, ring[r], ring[(r + 1) % R]);
     }
     if (st < nst) stage(st, ring[0], ring[1]);
-    if (st + 1 < nst) stage(st + 1, ring[1], ring[2]);
-    if (R == 4 && st + 2 < nst) stage(st + 2, ring[2], ring[3]);
+    if (R == 3 && st + 1 < nst) stage(st + 1, ring[1], ring[2]);
     wait_stage<0>();
     stage_barrier();
 }
@@ -385,9 +397,50 @@ __device__ __forceinline__ int64_t dealt_tile()
     return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
 }
 
-// Logits of one 256-label x TN-row tile.  GRAD = false: the tile's (maximum,
-// sum of exponentials) per row.  GRAD = true: D = exp(z - lse) of the piece
-// of labels [l0, l0 + Lc), without the labels' own terms.
+// Stores a wave's 128 x 64 tile as 64 rows (its columns) of 128 elements of the
+// type, value(mt, nt, e) each, through 8 KB of LDS: an accumulator holds runs
+// of four elements of a row, and stored as they lie those are 8-byte writes
+// to 64 places per instruction.  Staged, an instruction writes four runs of
+// 256 bytes.  Element run 8 c .. of row r sits in piece c ^ r % 16 of the
+// row, its 8-byte halves exchanged for r >= 16 (no bank meets twice).
+// put(r, c, v): 16 bytes of row r (0..63), piece c (0..15).
+template <int DT, class Value, class Put>
+__device__ __forceinline__ void store_rows(uint16_t* stage, int lane, Value&& value, Put&& put)
+{
+    const int r32 = lane & 31, hl = lane >> 5;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        wave_sync();
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<u32x2_t*>(stage + 128 * r32 + 8 * ((4 * mt + g) ^ (r32 & 15)) + 4 * (hl ^ (r32 >> 4))) =
+                    u32x2_t{pack2<DT>(value(mt, nt, 4 * g), value(mt, nt, 4 * g + 1)),
+                            pack2<DT>(value(mt, nt, 4 * g + 2), value(mt, nt, 4 * g + 3))};
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 4), c = lane & 15;
+            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stage + 128 * r + 8 * (c ^ (r & 15)));
+            put(32 * nt + r, c, i < 4 ? v : u32x4_t{v[2], v[3], v[0], v[1]});
+        }
+    }
+}
+// The same on the free ring: 8 KB per wave, the narrow tile's fourth wave in
+// the second buffer.
+template <int DT, int TN, class Value, class Put>
+__device__ __forceinline__ void store_tile(uint16_t* const (&ring)[3], Value&& value, Put&& put)
+{
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (TN == 256 || w < 3) store_rows<DT>(ring[0] + 4096 * w, lane, value, put);
+    else store_rows<DT>(ring[1], lane, value, put);
+}
+
+// Logits of one 256-label x TN-row tile, in units of log 2 from the
+// exponential on: GRAD = false: the tile's (maximum, sum of powers of two)
+// per row.  GRAD = true: D = softmax of the piece of labels [l0, l0 + Lc),
+// without the labels' own terms.
 template <int DT, int TN, bool GRAD>
 __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
 {
@@ -402,58 +455,59 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
     const int64_t m0 = l0 + mt0 * kTM;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
     f32x16_t acc[4][2];
-    tile_product<DT, TN, false, false>(A, m0, B, n0, (int)(a.Hp / kStage), ring, acc);
+    tile_product<DT, TN, false, false>(A, m0, B, n0, (int)(a.Hp / kStage<TN>), ring, acc);
 
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const int hl = lane >> 5, r32 = lane & 31;
+    if (m0 + kTM > a.L) {       // uniform: labels past the last one
+        const int live = (int)(a.L - m0) - 128 * wm - 4 * hl;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        const int64_t n = n0 + 64 * wn + 32 * nt + r32;
-        if constexpr (!GRAD) {
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (32 * mt + 8 * (e >> 2) + (e & 3) >= live) acc[mt][0][e] = acc[mt][1][e] = -INFINITY;
+    }
+    if constexpr (GRAD) {
+        float off[2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            const int64_t n = n0 + 64 * wn + 32 * nt + r32;
+            off[nt] = n < nv ? kDLog2<DT> - a.clse[n] : -INFINITY;
+        }
+        uint16_t* const dst = a.dz + dz_at(a, n0 + 64 * wn, mt0 * kTM + 128 * wm);
+        store_tile<DT, TN>(
+            ring,
+            [&](int mt, int nt, int e) { return __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, off[nt])); },
+            [&](int r, int c, u32x4_t v) { *reinterpret_cast<u32x4_t*>(dst + r * kTM + 8 * c) = v; });
+    } else {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
             float top = -INFINITY;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    if (m0 + 128 * wm + 32 * mt + 8 * (e >> 2) + 4 * hl + (e & 3) >= a.L) acc[mt][nt][e] = -INFINITY;
-                    top = fmaxf(top, acc[mt][nt][e]);
-                }
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            float sum = 0.f;
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[mt][nt][e]);
+            top = fmaxf(top, __shfl_xor(top, 32, 64)) * kLog2e;
             const float base = top == -INFINITY ? 0.f : top;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum += __builtin_amdgcn_exp2f((acc[mt][nt][e] - base) * kLog2e);
-            sum += __shfl_xor(sum, 32, 64);
+                for (int e = 0; e < 16; ++e)
+                    sum[mt] += __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, -base));
+            float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            all += __shfl_xor(all, 32, 64);
             if (hl == 0) {
                 red[wm][64 * wn + 32 * nt + r32][0] = top;
-                red[wm][64 * wn + 32 * nt + r32][1] = sum;
+                red[wm][64 * wn + 32 * nt + r32][1] = all;
             }
-        } else {
-            const float lse = n < nv ? a.clse[n] : 0.f, f = n < nv ? kDScale<DT> : 0.f;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const int64_t m = mt0 * kTM + 128 * wm + 32 * mt + 8 * g + 4 * hl;
-                    float d[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        d[i] = l0 + m + i < a.L ? __builtin_amdgcn_exp2f((acc[mt][nt][4 * g + i] - lse) * kLog2e) * f
-                                                : 0.f;
-                    *reinterpret_cast<u32x2_t*>(a.dz + dz_at(a, n, m)) =
-                        u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
-                }
         }
-    }
-    if constexpr (!GRAD) {
         __syncthreads();
         if (threadIdx.x < TN) {
             const float t0 = red[0][threadIdx.x][0], t1 = red[1][threadIdx.x][0];
             const float top = fmaxf(t0, t1), base = top == -INFINITY ? 0.f : top;
-            const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f((t0 - base) * kLog2e) +
-                              red[1][threadIdx.x][1] * __builtin_amdgcn_exp2f((t1 - base) * kLog2e);
+            const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f(t0 - base) +
+                              red[1][threadIdx.x][1] * __builtin_amdgcn_exp2f(t1 - base);
             *reinterpret_cast<f32x2_t*>(a.part + 2 * (mt0 * a.Bp + n0 + threadIdx.x)) = f32x2_t{top, sum};
         }
     }
@@ -472,7 +526,7 @@ __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
         for (int64_t t = r; t < tiles; t += 16) {
             const f32x2_t p = *reinterpret_cast<const f32x2_t*>(a.part + 2 * (t * a.Bp + i));
             const float nt = fmaxf(top, p[0]), base = nt == -INFINITY ? 0.f : nt;
-            sum = sum * __builtin_amdgcn_exp2f((top - base) * kLog2e) + p[1] * __builtin_amdgcn_exp2f((p[0] - base) * kLog2e);
+            sum = sum * __builtin_amdgcn_exp2f(top - base) + p[1] * __builtin_amdgcn_exp2f(p[0] - base);
             top = nt;
         }
     }
@@ -483,9 +537,9 @@ __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
         for (int k = 1; k < 16; ++k) top = fmaxf(top, st[k][c]);
         const float base = top == -INFINITY ? 0.f : top;
         sum = 0.f;
-        for (int k = 0; k < 16; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f((st[k][c] - base) * kLog2e);
-        const float lse = base + logf(sum);
-        a.clse[i] = lse;
+        for (int k = 0; k < 16; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f(st[k][c] - base);
+        const float lse2 = base + log2f(sum), lse = lse2 * kLn2;
+        a.clse[i] = lse2;
         a.lse[a.rows[i]] = lse;
         a.row_loss[a.rows[i]] = lse - a.hit[i];
     }
@@ -511,7 +565,7 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
         const int64_t l = a.y_col[p];
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
-        const float d = (__builtin_amdgcn_exp2f((z - lse) * kLog2e) - share) * kDScale<DT>;
+        const float d = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -lse)) - share) * kDScale<DT>;
         if (lane == 0) a.dz[dz_at(a, i, l - l0)] = (uint16_t)pack2<DT>(d, 0.f);
     }
 }
@@ -526,24 +580,16 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dw(SoftmaxArgs a, int64_
     const Operand A{a.hc, a.Hp, a.Hp, a.Bp};
     const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
     f32x16_t acc[4][2];
-    tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage - 1) / kStage, ring, acc);
+    tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage<TN> - 1) / kStage<TN>, ring, acc);
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const float f = a.scale / kDScale<DT>;
-    uint16_t* dW = reinterpret_cast<uint16_t*>(a.dW);
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        const int64_t l = l0 + n0 + 64 * wn + 32 * nt + (lane & 31);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t j = m0 + 128 * wm + 32 * mt + 8 * g + 4 * (lane >> 5);
-                if (l < a.L && j < a.H)
-                    *reinterpret_cast<u32x2_t*>(dW + l * a.H + j) =
-                        u32x2_t{pack2<DT>(acc[mt][nt][4 * g] * f, acc[mt][nt][4 * g + 1] * f),
-                                pack2<DT>(acc[mt][nt][4 * g + 2] * f, acc[mt][nt][4 * g + 3] * f)};
-            }
-    }
+    uint16_t* const dW = reinterpret_cast<uint16_t*>(a.dW);
+    const int64_t l = l0 + n0 + 64 * wn, j = m0 + 128 * wm;
+    store_tile<DT, TN>(
+        ring, [&](int mt, int nt, int e) { return acc[mt][nt][e] * f; },
+        [&](int r, int c, u32x4_t v) {
+            if (l + r < a.L && j + 8 * c < a.H) stg_stream(dW + (l + r) * a.H + j + 8 * c, v);
+        });
 }
 
 // Label ranges that the feature gradient of nv rows is split into: as many
@@ -570,11 +616,12 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dh(SoftmaxArgs a, int64_
     const int64_t len = (a.Lc / splits + kTM - 1) / kTM * kTM;
     const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;       // labels of the piece
     int64_t k0 = s * len, k1 = s == splits - 1 ? a.Lc : k0 + len;
-    if (k1 > (live + kStage - 1) / kStage * kStage) k1 = (live + kStage - 1) / kStage * kStage;
+    const int64_t end = (live + kStage<TN> - 1) / kStage<TN> * kStage<TN>;   // no stage starts past the last label
+    if (k1 > end) k1 = end;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W) + (l0 + k0) * a.ldw, a.ldw, a.H, live - k0};
     const Operand B{a.dz + dz_at(a, 0, k0), kTM, a.Bp, a.Lc - k0, a.Bp * kTM};
     f32x16_t acc[4][2];
-    tile_product<DT, TN, true, false, true>(A, m0, B, n0, (int)((k1 - k0) / kStage), ring, acc);
+    tile_product<DT, TN, true, false, true>(A, m0, B, n0, (int)((k1 - k0) / kStage<TN>), ring, acc);
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {

@@ -271,8 +271,8 @@ struct SoftmaxArgs {
     int32_t* rows;          // Bp
     int32_t* rank;          // B, -1 for rows without labels
     float* hit;             // Bp: mean logit of the row's labels
-    float* clse;            // Bp: log-sum-exp by rank
-    float* part;            // label tiles x Bp x (max, sum)
+    float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
+    float* part;            // label tiles x Bp x (max, sum), units of log 2
     uint16_t* hc;           // Bp x Hp
     uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
     float* dhp;             // partials of dh, at most max(dh_slots, tiles) tiles of 256 x tn
