@@ -57,7 +57,7 @@ struct SoftmaxLayout {
         Lr = round_up(L, kSmLabelTile);
         const int64_t most = (256LL << 20) / (2 * Bp) / kSmLabelTile * kSmLabelTile;
         want = balanced(most < kSmLabelTile ? kSmLabelTile : most);
-        const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / tn), slots = sm_dh_slots(tn);
+        const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / 128);
         size_t at = 0;
         auto take = [&](size_t n) {
             const size_t o = at;
@@ -67,11 +67,11 @@ struct SoftmaxLayout {
         nv = take(4);
         rows = take((size_t)Bp * 4);
         rank = take((size_t)B * 4);
-        hit = take((size_t)Bp * 4);
+        hit = take((size_t)Bp * 4 * kSmSlices);
         clse = take((size_t)Bp * 4);
         part = take((size_t)(Lr / kSmLabelTile) * (size_t)Bp * 8);
         hc = take((size_t)Bp * (size_t)Hp * 2);
-        dhp = grad ? take((size_t)(tiles > slots ? tiles : slots) * (size_t)(tn * kSmLabelTile) * 4) : at;
+        dhp = grad ? take((size_t)(tiles > kSmDhSlots ? tiles : kSmDhSlots) * (size_t)(128 * kSmLabelTile) * 4) : at;
         dz = at;
     }
     int64_t balanced(int64_t most) const
@@ -113,7 +113,7 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.h = h; a.W = W; a.y_rowptr = y_rowptr; a.y_col = y_col;
     a.B = B; a.H = H; a.L = L; a.ldh = ldh; a.ldw = ldw; a.scale = scale;
     a.dW = dW; a.dh = dh; a.row_loss = row_loss; a.lse = lse; a.loss = loss;
-    a.tn = l.tn; a.Bp = l.Bp; a.Hp = l.Hp; a.dh_slots = sm_dh_slots(l.tn);
+    a.tn = l.tn; a.Bp = l.Bp; a.Hp = l.Hp;
     a.Lc = l.want;
     if (grad && workspace_bytes < l.total(l.want, true))
         a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / (2 * (size_t)l.Bp)) / kSmLabelTile * kSmLabelTile);

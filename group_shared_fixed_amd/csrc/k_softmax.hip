@@ -103,8 +103,9 @@ __device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* 
     return wave_sum(s);
 }
 
-// Workgroup i: row of rank i into hc (zeros past nv and past H), and the
-// mean logit of its labels.
+// Workgroup (i, y): the mean logit of the labels 4 y .., 16 at a time, of rank
+// i's row (its share of it: hit[y][i]); y = 0 also copies the row into hc
+// (zeros past nv and past H).
 template <int DT>
 __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
 {
@@ -114,19 +115,21 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
     const bool live = i < *a.nv;
     const int64_t b = live ? a.rows[i] : 0;
     const uint16_t* src = reinterpret_cast<const uint16_t*>(a.h) + b * a.ldh;
-    for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048)
-        *reinterpret_cast<u32x4_t*>(a.hc + i * a.Hp + j) =
-            live && j < a.H ? ldg16(src + j) : u32x4_t{0u, 0u, 0u, 0u};
+    if (blockIdx.y == 0)
+        for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048)
+            *reinterpret_cast<u32x4_t*>(a.hc + i * a.Hp + j) =
+                live && j < a.H ? ldg16(src + j) : u32x4_t{0u, 0u, 0u, 0u};
     if (!live) return;
     const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
     float s = 0.f;
-    for (int p = p0 + w; p < p1; p += 4) {
+    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * kSmSlices) {
         const int64_t l = a.y_col[p];
         if (l >= 0 && l < a.L) s += wave_dot<DT>(a, src, l, lane);
     }
     if (lane == 0) sh[w] = s;
     __syncthreads();
-    if (threadIdx.x == 0) a.hit[i] = ((sh[0] + sh[1]) + (sh[2] + sh[3])) / (float)(p1 - p0);
+    if (threadIdx.x == 0)
+        a.hit[blockIdx.y * a.Bp + i] = ((sh[0] + sh[1]) + (sh[2] + sh[3])) / (float)(p1 - p0);
 }
 
 // An operand tile: T (256 or 128) tile rows by one stage of ST contraction elements.
@@ -513,45 +516,61 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
     }
 }
 
-// Log-sum-exp of 16 ranks per workgroup from the tiles' pairs, 16 threads
-// per rank; the results by row (0 for rows without labels).
+// Log-sum-exp of 8 ranks per workgroup from the tiles' pairs, 32 threads per
+// rank; the results by row (0 for rows without labels).
 __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
 {
-    __shared__ float st[16][17], ss[16][17];
-    const int c = threadIdx.x & 15, r = threadIdx.x >> 4;
-    const int64_t i = (int64_t)blockIdx.x * 16 + c;
+    __shared__ float st[32][9], ss[32][9];
+    const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+    const int64_t i = (int64_t)blockIdx.x * 8 + c;
     const int nv = *a.nv;
     float top = -INFINITY, sum = 0.f;
     if (i < nv) {
-        for (int64_t t = r; t < tiles; t += 16) {
-            const f32x2_t p = *reinterpret_cast<const f32x2_t*>(a.part + 2 * (t * a.Bp + i));
-            const float nt = fmaxf(top, p[0]), base = nt == -INFINITY ? 0.f : nt;
-            sum = sum * __builtin_amdgcn_exp2f(top - base) + p[1] * __builtin_amdgcn_exp2f(p[0] - base);
-            top = nt;
+        constexpr int U = 8;
+        for (int64_t t0 = r; t0 < tiles; t0 += 32 * U) {
+            f32x2_t p[U];
+            float m = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t t = t0 + 32 * u;
+                p[u] = t < tiles ? *reinterpret_cast<const f32x2_t*>(a.part + 2 * (t * a.Bp + i)) : f32x2_t{-INFINITY, 0.f};
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) m = fmaxf(m, p[u][0]);
+            const float base = m == -INFINITY ? 0.f : m;
+            sum *= __builtin_amdgcn_exp2f(top - base);
+#pragma unroll
+            for (int u = 0; u < U; ++u) sum += p[u][1] * __builtin_amdgcn_exp2f(p[u][0] - base);
+            top = m;
         }
     }
     st[r][c] = top;
     ss[r][c] = sum;
     __syncthreads();
     if (r == 0 && i < nv) {
-        for (int k = 1; k < 16; ++k) top = fmaxf(top, st[k][c]);
+#pragma unroll
+        for (int k = 1; k < 32; ++k) top = fmaxf(top, st[k][c]);
         const float base = top == -INFINITY ? 0.f : top;
         sum = 0.f;
-        for (int k = 0; k < 16; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f(st[k][c] - base);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f(st[k][c] - base);
         const float lse2 = base + log2f(sum), lse = lse2 * kLn2;
+        float hit = 0.f;
+#pragma unroll
+        for (int k = 0; k < kSmSlices; ++k) hit += a.hit[k * a.Bp + i];
         a.clse[i] = lse2;
         a.lse[a.rows[i]] = lse;
-        a.row_loss[a.rows[i]] = lse - a.hit[i];
+        a.row_loss[a.rows[i]] = lse - hit;
     }
     // rows without labels
-    if (threadIdx.x < 16) {
-        const int64_t b = (int64_t)blockIdx.x * 16 + threadIdx.x;
+    if (threadIdx.x < 8) {
+        const int64_t b = (int64_t)blockIdx.x * 8 + threadIdx.x;
         if (b < a.B && a.rank[b] < 0) a.lse[b] = a.row_loss[b] = 0.f;
     }
 }
 
-// The labels' own entries of D in the piece [l0, l0 + Lc): one workgroup per
-// rank.  The logit is formed again here, in fp32.
+// The labels' own entries of D in the piece [l0, l0 + Lc): workgroups as in
+// k_sm_gather.  The logit is formed again here, in fp32.
 template <int DT>
 __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
 {
@@ -561,7 +580,7 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
     const int64_t b = a.rows[i];
     const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
     const float share = 1.0f / (float)(p1 - p0), lse = a.clse[i];
-    for (int p = p0 + w; p < p1; p += 4) {
+    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * kSmSlices) {
         const int64_t l = a.y_col[p];
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
@@ -592,11 +611,17 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dw(SoftmaxArgs a, int64_
         });
 }
 
+// The feature gradient has few tiles and a long contraction: it takes the
+// narrow tile at every batch, two workgroups per CU, so that the label ranges
+// its tiles are split into fill the grid evenly (100 tiles in 5 ranges at
+// 3100 live rows: 216 us a piece of 32768 labels, 257 us on the wide tile).
+constexpr int kDhRows = 128;
+
 // Label ranges that the feature gradient of nv rows is split into: as many
 // as fill the grid once, in whole blocks of D.
 __device__ __forceinline__ int64_t dh_splits(const SoftmaxArgs& a, int64_t tiles)
 {
-    int64_t s = a.dh_slots / tiles;
+    int64_t s = kSmDhSlots / tiles;
     if (s > a.Lc / kTM) s = a.Lc / kTM;
     return s < 1 ? 1 : s;
 }
@@ -659,24 +684,35 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
         return;
     }
     if (!grad) return;
+    // 32 runs of eight columns per workgroup, eight threads each over the partials
+    __shared__ float part[8][32][9];
     const int64_t per = a.H / 8, n = a.B * per;
     const float f = a.scale / kDScale<DT>;
-    const int64_t nvt = (*a.nv + a.tn - 1) / a.tn;
+    const int64_t nvt = (*a.nv + kDhRows - 1) / kDhRows;
     const int64_t splits = nvt ? dh_splits(a, ncols * nvt) : 0;
-    for (int64_t t = (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x; t < n; t += (int64_t)(gridDim.x - 1) * 256) {
-        const int64_t b = t / per, j = 8 * (t % per), i = a.rank[b];
-        float v[8];
+    const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int64_t t = (int64_t)(blockIdx.x - 1) * 32 + c;
+    const int64_t b = t / per, j = 8 * (t % per), i = t < n ? a.rank[b] : -1;
+    float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.f;
-        if (i >= 0) {
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    if (i >= 0) {
 #pragma unroll 4
-            for (int64_t s = 0; s < splits; ++s) {
-                float w[8];
-                widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * a.tn + i) * a.Hp + j, 8), w);
+        for (int64_t s = g; s < splits; s += 8) {
+            float w[8];
+            widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * kDhRows + i) * a.Hp + j, 8), w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += w[e];
-            }
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[g][c][e] = v[e];
+    __syncthreads();
+    if (g == 0 && t < n) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += part[k][c][e];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= f;
         store8<DT>(a.dh, b * a.H + j, 8, v);
@@ -689,22 +725,22 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
     constexpr int NT = kThreads<TN>;
     const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
     k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
-    k_sm_gather<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a);
+    k_sm_gather<DT><<<dim3((unsigned)a.Bp, kSmSlices), 256, 0, s>>>(a);
     k_sm_logits<DT, TN, false><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0);
-    k_sm_lse<<<(unsigned)((a.Bp + 15) / 16), 256, 0, s>>>(a, tiles);
+    k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
     if (grad) {
-        const int64_t dh_grid = ncols * nrt > a.dh_slots ? ncols * nrt : a.dh_slots;
+        const int64_t dh_tiles = ncols * (a.Bp / kDhRows), dh_grid = dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots;
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
             k_sm_logits<DT, TN, true><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0);
-            k_sm_labels<DT><<<(unsigned)a.Bp, 256, 0, s>>>(a, l0);
+            k_sm_labels<DT><<<dim3((unsigned)a.Bp, kSmSlices), 256, 0, s>>>(a, l0);
             k_sm_dw<DT, TN><<<(unsigned)((live + TN - 1) / TN * ncols), NT, 0, s>>>(a, l0, ncols);
-            k_sm_dh<DT, TN><<<(unsigned)dh_grid, NT, 0, s>>>(a, l0, ncols, l0 == 0);
+            k_sm_dh<DT, kDhRows><<<(unsigned)dh_grid, kThreads<kDhRows>, 0, s>>>(a, l0, ncols, l0 == 0);
         }
     }
-    const int64_t blocks = grad ? (a.B * (a.H / 8) + 255) / 256 : 0;
-    k_sm_finish<DT><<<(unsigned)(1 + (blocks > 4096 ? 4096 : blocks)), 256, 0, s>>>(a, grad, ncols);
+    const int64_t blocks = grad ? (a.B * (a.H / 8) + 31) / 32 : 0;
+    k_sm_finish<DT><<<(unsigned)(1 + blocks), 256, 0, s>>>(a, grad, ncols);
 }
 
 template <int DT>

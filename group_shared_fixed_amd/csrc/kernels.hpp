@@ -266,21 +266,20 @@ struct SoftmaxArgs {
     int64_t tn;             // rows per tile: sm_row_tile(B)
     int64_t Bp, Hp;         // B and H rounded up to tn and 64
     int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
-    int64_t dh_slots;       // workgroups that fill the chip with feature-gradient tiles
     int32_t* nv;
     int32_t* rows;          // Bp
     int32_t* rank;          // B, -1 for rows without labels
-    float* hit;             // Bp: mean logit of the row's labels
+    float* hit;             // kSmSlices x Bp: shares of the mean logit of the row's labels
     float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
     float* part;            // label tiles x Bp x (max, sum), units of log 2
     uint16_t* hc;           // Bp x Hp
     uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
-    float* dhp;             // partials of dh, at most max(dh_slots, tiles) tiles of 256 x tn
+    float* dhp;             // partials of dh, at most max(kSmDhSlots, tiles) tiles of 256 x 128
 };
 constexpr int64_t kSmLabelTile = 256;
 constexpr int64_t sm_row_tile(int64_t B) { return B > 128 ? 256 : 128; }
-// one workgroup of the wide tile per CU, two of the narrow one
-constexpr int64_t sm_dh_slots(int64_t tn) { return tn == 256 ? 256 : 512; }
+constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
+constexpr int kSmSlices = 4;           // workgroups that share a row's labels
 void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s);
 
 }  // namespace haste
