@@ -6,10 +6,8 @@
 // against fp64 at H = 768: 3e-8 of the result's norm).  The 8-bit matrix
 // products keep fewer bits of the terms they add (1.5e-5 there), past what
 // an fp32 output stands for.
-//
-// One wave per 16 x 16 tile of (labels, rows), operands straight from memory.
-#include "elem.hpp"
 #include "kernels.hpp"
+#include "tile.hpp"
 
 namespace haste {
 namespace {
@@ -21,7 +19,9 @@ __device__ __forceinline__ void widen16(u32x4_t c, u32x4_t& lo, u32x4_t& hi)
     hi = widen_w8(u32x2_t{c[2], c[3]}, 1.0f);
 }
 
-__global__ __launch_bounds__(256) void k_score(ScoreArgs a)
+// Few rows: one pass over the weights.  One wave per 16 x 16 tile of (labels,
+// rows), operands straight from memory.
+__global__ __launch_bounds__(256) void k_score_few(ScoreArgs a)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r16 = lane & 15, q = lane >> 4;
     const int64_t l0 = ((int64_t)blockIdx.x * 4 + w) * 16, b0 = (int64_t)blockIdx.y * 16;
@@ -49,12 +49,153 @@ __global__ __launch_bounds__(256) void k_score(ScoreArgs a)
     }
 }
 
+// Many rows: tiles of 128 rows x 256 labels by four waves of 128 x 64, two
+// workgroups per CU, so that one's stores run under the other's products.
+// The codes move into a ring of three LDS stages of 64 (24 KB each) as they
+// are, half the bytes of bf16, and are widened between LDS and the products.
+// A lane's 16-byte read is two operands: any assignment of contraction
+// indices to steps works as long as both sides use the same.
+// RAGGED: H % 64 != 0; the pieces past H, which repeat the last one, are
+// zeroed on the features' side.
+constexpr int kScRows = 128, kScLabels = 256, kScStage = 32;     // stage in 16-bit units
+template <bool RAGGED>
+__global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
+{
+    constexpr int kBuf = (kScRows + kScLabels) * kScStage;
+    __shared__ __attribute__((aligned(1024))) uint16_t ring0[kBuf], ring1[kBuf], ring2[kBuf];
+    uint16_t* const ring[3] = {ring0, ring1, ring2};
+    const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, hl = lane >> 5;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    // label tiles by the row tiles in turn: a weight tile is read once per XCD
+    const int64_t nrt = (a.B + kScRows - 1) / kScRows, t = dealt_tile();
+    const int64_t b0 = t % nrt * kScRows, l0 = t / nrt * kScLabels;
+    const int64_t ld = a.H / 2;
+    const Operand A{reinterpret_cast<const uint16_t*>(a.hq), ld, a.B, ld}, B{reinterpret_cast<const uint16_t*>(a.Wq), ld, a.L, ld};
+    using MA = Mover<kScRows, false, kScStage, 256>;
+    using MB = Mover<kScLabels, false, kScStage, 256>;
+    const MA ma(A, b0, w, lane);
+    const MB mb(B, l0, w, lane);
+    const int nst = (int)((ld + kScStage - 1) / kScStage);
+    auto move = [&](int st, uint16_t* buf) {
+        const int s = st < nst ? st : nst - 1;       // past the end: into a buffer nobody reads
+        ma.move(s, buf, w);
+        mb.move(s, buf + kScRows * kScStage, w);
+    };
+    f32x16_t acc[4][2];
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = f32x16_t{};
+    u32x4_t ra[2][4], rb[2][2];
+    auto read = [&](const uint16_t* buf, int j) {
+        fragments<kScLabels, false, kScStage>(buf + kScRows * kScStage, 2 * w, j, lane, rb[j]);
+        fragments<kScRows, false, kScStage>(buf, 0, j, lane, ra[j]);
+    };
+    auto products = [&](int st, int j) {
+        u32x4_t bf[2][2];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) widen16(rb[j][nt], bf[0][nt], bf[1][nt]);
+        const bool live = !RAGGED || 64 * st + 16 * (2 * j + hl) < a.H;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            u32x4_t r = ra[j][mt], af[2];
+            if (RAGGED && !live) r = u32x4_t{0u, 0u, 0u, 0u};
+            widen16(r, af[0], af[1]);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<HASTE_BF16>(af[s], bf[s][nt], acc[mt][nt]);
+        }
+    };
+    auto stage = [&](int st, uint16_t* cur, const uint16_t* next) {
+        read(cur, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        products(st, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        wait_stage<MA::N + MB::N>();
+        stage_barrier();
+        move(st + 3, cur);
+        read(next, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        products(st, 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    move(0, ring0);
+    move(1, ring1);
+    move(2, ring2);
+    wait_stage<2 * (MA::N + MB::N)>();
+    stage_barrier();
+    read(ring0, 0);
+    int st = 0;
+    for (; st + 3 <= nst; st += 3) {
+#pragma unroll
+        for (int r = 0; r < 3; ++r) stage(st + r, ring[r], ring[(r + 1) % 3]);
+    }
+    if (st < nst) stage(st, ring0, ring1);
+    if (st + 1 < nst) stage(st + 1, ring1, ring2);
+    wait_stage<0>();             // moves past the end: none may outlive the workgroup
+
+    stage_barrier();
+    // Z leaves through LDS, 16 rows x 64 labels of a wave at a time (4 KB), so
+    // that an instruction stores four runs of 256 bytes; as the accumulators
+    // lie, 128 bytes of two rows per instruction, it took 424 us instead of
+    // 298 at 2048 x 89088 x 768 (the products alone take 224)
+    float* const sg = reinterpret_cast<float*>(ring0) + 1024 * w;     // 16 rows x 64 labels
+    float sw[2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const int64_t l = l0 + 64 * w + 32 * nt + r32;
+        sw[nt] = l < a.L ? a.ws[l] : 0.f;
+    }
+    const bool vec = (a.L & 3) == 0;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            wave_sync();
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int r = 8 * g + 4 * hl + i;
+                        sg[64 * r + 32 * nt + r32] = acc[mt][nt][8 * hf + 4 * g + i] * sw[nt];
+                    }
+            wave_sync();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * i + (lane >> 4), c = 4 * (lane & 15);
+                const int64_t b = b0 + 32 * mt + 16 * hf + r, l = l0 + 64 * w + c;
+                f32x4_t v = *reinterpret_cast<const f32x4_t*>(sg + 64 * r + c);
+                if (b >= a.B) continue;
+                v *= a.hs[b];
+                float* const z = a.Z + b * a.L + l;
+                if (vec && l + 4 <= a.L) {
+                    stg_stream(z, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (l + k < a.L) z[k] = v[k];
+                }
+            }
+        }
+}
+
+// Rows up to which the weights are streamed instead of tiled.
+constexpr int64_t kScFew = 32;
+
 }  // namespace
 
 void launch_score(const ScoreArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.L + 63) / 64), (unsigned)((a.B + 15) / 16));
-    k_score<<<grid, 256, 0, s>>>(a);
+    if (a.B <= kScFew) {
+        k_score_few<<<dim3((unsigned)((a.L + 63) / 64), (unsigned)((a.B + 15) / 16)), 256, 0, s>>>(a);
+        return;
+    }
+    const int64_t tiles = (a.B + kScRows - 1) / kScRows * ((a.L + kScLabels - 1) / kScLabels);
+    if (a.H % 64 == 0) k_score_tiles<false><<<(unsigned)tiles, 256, 0, s>>>(a);
+    else k_score_tiles<true><<<(unsigned)tiles, 256, 0, s>>>(a);
 }
 
 }  // namespace haste

@@ -83,7 +83,7 @@ def test_quantize_and_score_refuse(L):
         assert score(**{k: None}) == NULL and score(**{k: MIS}) == ALIGN
     assert score(B=0) == DIM and score(H=0) == DIM and score(n=0) == DIM
     assert score(H=24) == UNSUP and score(H=1 << 15) == UNSUP and score(B=(1 << 20) + 1) == UNSUP
-    assert score(n=2**31 - 64) == UNSUP
+    assert score(n=2**31 - 64) == UNSUP and score(B=1 << 20, n=2**31 - 65) == UNSUP
 
 
 def soft(L, grad=True, h=A, W=A, rp=A, col=A, scale=1.0, dW=A, dh=A, rl=A, lse=A, loss=A, B=40, H=64, n=1000, ldh=64,
