@@ -72,6 +72,55 @@ __global__ __launch_bounds__(1024) void k_sm_rows(const int32_t* __restrict__ ro
     if (t == 1023) *nv = cnt[1023];
 }
 
+// Batches of up to kFewRows find their ranks in the gather itself (each of
+// its workgroups counts), one launch less.
+constexpr int64_t kFewRows = 1024;
+// The row of rank i (or -1) and the number of ranks, by the whole workgroup of
+// 256; PUBLISH also writes rows, rank and nv.
+template <bool PUBLISH>
+__device__ __forceinline__ int64_t find_rank(const SoftmaxArgs& a, int64_t i, int& nv)
+{
+    __shared__ int32_t cnt[4], found;
+    const int t = threadIdx.x, w = t >> 6;
+    int32_t p[5];
+    const int64_t b0 = 4 * (int64_t)t;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) p[k] = a.y_rowptr[b0 + k < a.B ? b0 + k : a.B];
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += p[k + 1] > p[k];
+    int at = n;                                   // inclusive scan over the wave
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(at, o, 64);
+        if ((t & 63) >= o) at += v;
+    }
+    if ((t & 63) == 63) cnt[w] = at;
+    if (t == 0) found = -1;
+    __syncthreads();
+    int before = 0;
+    nv = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        before += k < w ? cnt[k] : 0;
+        nv += cnt[k];
+    }
+    at += before - n;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const bool has = p[k + 1] > p[k];
+        if (has && at == i) found = (int32_t)(b0 + k);
+        if (PUBLISH && b0 + k < a.B) {
+            a.rank[b0 + k] = has ? at : -1;
+            if (has) a.rows[at] = (int32_t)(b0 + k);
+        }
+        at += has;
+    }
+    if (PUBLISH && t == 0) *a.nv = nv;
+    __syncthreads();
+    return found;
+}
+
 // <hc[i], W[l]> by one wave, fp32.
 template <int DT>
 __device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* hrow, int64_t l, int lane)
@@ -90,15 +139,23 @@ __device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* 
 // Workgroup (i, y): the mean logit of the labels 4 y .., 16 at a time, of rank
 // i's row (its share of it: hit[y][i]); y = 0 also copies the row into hc
 // (zeros past nv and past H).
-template <int DT>
+template <int DT, bool FEW>
 __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
 {
     __shared__ float sh[4];
     const int64_t i = blockIdx.x;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const bool live = i < *a.nv;
-    const int64_t b = live ? a.rows[i] : 0;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.h) + b * a.ldh;
+    int64_t b;
+    bool live;
+    if constexpr (FEW) {
+        int nv;
+        b = blockIdx.x == 0 && blockIdx.y == 0 ? find_rank<true>(a, i, nv) : find_rank<false>(a, i, nv);
+        live = b >= 0;
+    } else {
+        live = i < *a.nv;
+        b = live ? a.rows[i] : 0;
+    }
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.h) + (live ? b : 0) * a.ldh;
     if (blockIdx.y == 0)
         for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048)
             *reinterpret_cast<u32x4_t*>(a.hc + i * a.Hp + j) =
@@ -401,10 +458,10 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
 
 // dW of one tile of 256 columns x TN labels of the piece.
 template <int DT, int TN>
-__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
+__device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_t ncols, int64_t t,
+                                        uint16_t* const (&ring)[3])
 {
-    HASTE_SM_RING(TN)
-    const int64_t t = dealt_tile(), m0 = t % ncols * kTM, n0 = t / ncols * TN;
+    const int64_t m0 = t % ncols * kTM, n0 = t / ncols * TN;
     const int nv = *a.nv;
     const Operand A{a.hc, a.Hp, a.Hp, a.Bp};
     const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
@@ -440,12 +497,12 @@ __device__ __forceinline__ int64_t dh_splits(const SoftmaxArgs& a, int64_t tiles
 // labels, added to (or, for the first piece, stored in) that range's partial
 // (ranges x live rows, in whole tiles, x Hp).
 template <int DT, int TN>
-__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
+__device__ __forceinline__ void dh_tile(const SoftmaxArgs& a, int64_t l0, int64_t ncols, int first, int64_t d,
+                                        uint16_t* const (&ring)[3])
 {
-    HASTE_SM_RING(TN)
     const int64_t nvt = (*a.nv + TN - 1) / TN, tiles = ncols * nvt;
     if (tiles == 0) return;
-    const int64_t splits = dh_splits(a, tiles), d = dealt_tile(), s = d / tiles, t = d % tiles;
+    const int64_t splits = dh_splits(a, tiles), s = d / tiles, t = d % tiles;
     if (s >= splits) return;
     const int64_t m0 = t % ncols * kTM, n0 = t / ncols * TN;
     const int64_t len = (a.Lc / splits + kTM - 1) / kTM * kTM;
@@ -473,6 +530,33 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_dh(SoftmaxArgs a, int64_
                 *o = v;
             }
     }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads<256>, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
+{
+    HASTE_SM_RING(256)
+    dw_tile<DT, 256>(a, l0, ncols, dealt_tile(), ring);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads<kDhRows>, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
+{
+    HASTE_SM_RING(kDhRows)
+    dh_tile<DT, kDhRows>(a, l0, ncols, first, dealt_tile(), ring);
+}
+
+// Both gradients of a piece in one launch, for batches of one row tile: the
+// products are short there, dW is bound by its stores and dh by its reads of
+// W, and run together they share the memory's time.  Workgroups
+// [0, dh_grid) take dh.
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_sm_grads(SoftmaxArgs a, int64_t l0, int64_t ncols, int first,
+                                                     uint32_t dh_grid)
+{
+    HASTE_SM_RING(128)
+    if (blockIdx.x < dh_grid) dh_tile<DT, 128>(a, l0, ncols, first, dealt_tile(blockIdx.x, dh_grid), ring);
+    else dw_tile<DT, 128>(a, l0, ncols, dealt_tile(blockIdx.x - dh_grid, gridDim.x - dh_grid), ring);
 }
 
 // dh by row from the partials (0 for rows without labels); workgroup 0 also
@@ -534,19 +618,29 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
 {
     constexpr int NT = kThreads<TN>;
     const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
-    k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
-    k_sm_gather<DT><<<dim3((unsigned)a.Bp, kSmSlices), 256, 0, s>>>(a);
+    const dim3 by_rank((unsigned)a.Bp, kSmSlices);
+    if (a.B <= kFewRows) {
+        k_sm_gather<DT, true><<<by_rank, 256, 0, s>>>(a);
+    } else {
+        k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
+        k_sm_gather<DT, false><<<by_rank, 256, 0, s>>>(a);
+    }
     k_sm_logits<DT, TN, false><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0);
     k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
     if (grad) {
-        const int64_t dh_tiles = ncols * (a.Bp / kDhRows), dh_grid = dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots;
+        const int64_t dh_tiles = ncols * (a.Bp / kDhRows), dh_grid = ((dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots) + 7) / 8 * 8;
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
             k_sm_logits<DT, TN, true><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0);
-            k_sm_labels<DT><<<dim3((unsigned)a.Bp, kSmSlices), 256, 0, s>>>(a, l0);
-            k_sm_dw<DT, TN><<<(unsigned)((live + TN - 1) / TN * ncols), NT, 0, s>>>(a, l0, ncols);
-            k_sm_dh<DT, kDhRows><<<(unsigned)dh_grid, kThreads<kDhRows>, 0, s>>>(a, l0, ncols, l0 == 0);
+            k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
+            const int64_t dw_tiles = (live + TN - 1) / TN * ncols;
+            if constexpr (TN == 256) {
+                k_sm_dw<DT><<<(unsigned)dw_tiles, NT, 0, s>>>(a, l0, ncols);
+                k_sm_dh<DT><<<(unsigned)dh_grid, kThreads<kDhRows>, 0, s>>>(a, l0, ncols, l0 == 0);
+            } else {
+                k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), NT, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);
+            }
         }
     }
     const int64_t blocks = grad ? (a.B * (a.H / 8) + 31) / 32 : 0;

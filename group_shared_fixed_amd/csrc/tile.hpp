@@ -190,10 +190,11 @@ __device__ __forceinline__ void fragments(const uint16_t* tile, int x0, int s, i
 
 // Tile of this workgroup: ids go round-robin over the 8 XCDs, so each XCD is
 // dealt one run of neighbouring tiles, whose operands meet in its L2.
-__device__ __forceinline__ int64_t dealt_tile()
+__device__ __forceinline__ int64_t dealt_tile(uint32_t b, uint32_t nb)
 {
-    const uint32_t nb = gridDim.x, b = blockIdx.x, per = nb / 8;
+    const uint32_t per = nb / 8;
     return b < per * 8 ? (b & 7) * per + (b >> 3) : b;
 }
+__device__ __forceinline__ int64_t dealt_tile() { return dealt_tile(blockIdx.x, gridDim.x); }
 
 }  // namespace haste
