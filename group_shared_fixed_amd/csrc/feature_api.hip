@@ -48,7 +48,7 @@ int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_d
 // from the bytes that are left.
 struct SoftmaxLayout {
     int64_t tn, Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
-    size_t nv, rows, rank, hit, clse, part, hc, dhp, dz;
+    size_t nv, rows, rank, hit, clse, part, rest, hc, dhp, dz;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
     {
         tn = sm_row_tile(B);
@@ -70,6 +70,7 @@ struct SoftmaxLayout {
         hit = take((size_t)Bp * 4 * kSmSlices);
         clse = take((size_t)Bp * 4);
         part = take((size_t)(Lr / kSmLabelTile) * (size_t)Bp * 8);
+        rest = grad ? take((size_t)(Bp * kSmRest) * 4) : at;
         hc = take((size_t)Bp * (size_t)Hp * 2);
         dhp = grad ? take((size_t)(tiles > kSmDhSlots ? tiles : kSmDhSlots) * (size_t)(128 * kSmLabelTile) * 4) : at;
         dz = at;
@@ -79,7 +80,9 @@ struct SoftmaxLayout {
         const int64_t n = (Lr + most - 1) / most;
         return round_up((Lr + n - 1) / n, kSmLabelTile);
     }
-    size_t total(int64_t Lc, bool grad) const { return dz + (grad ? (size_t)Bp * (size_t)Lc * 2 : 0); }
+    // per block of 256 labels of a piece: its part of D, its list and the list's length
+    size_t block() const { return (size_t)Bp * kSmLabelTile * 2 + kSmList * sizeof(u32x4_t) + sizeof(int32_t); }
+    size_t total(int64_t Lc, bool grad) const { return dz + (grad ? align256((size_t)(Lc / kSmLabelTile) * block()) : 0); }
 };
 
 int check_softmax_shape(int64_t B, int64_t H, int64_t L)
@@ -116,7 +119,7 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.tn = l.tn; a.Bp = l.Bp; a.Hp = l.Hp;
     a.Lc = l.want;
     if (grad && workspace_bytes < l.total(l.want, true))
-        a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / (2 * (size_t)l.Bp)) / kSmLabelTile * kSmLabelTile);
+        a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / l.block()) * kSmLabelTile);
     a.nv = (int32_t*)(w + l.nv);
     a.rows = (int32_t*)(w + l.rows);
     a.rank = (int32_t*)(w + l.rank);
@@ -125,7 +128,11 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.part = (float*)(w + l.part);
     a.hc = (uint16_t*)(w + l.hc);
     a.dhp = (float*)(w + l.dhp);
+    a.rest = (float*)(w + l.rest);
+    a.rest_cap = l.Bp * kSmRest;
     a.dz = (uint16_t*)(w + l.dz);
+    a.list = (u32x4_t*)(a.dz + l.Bp * a.Lc);
+    a.count = (int32_t*)(a.list + a.Lc / kSmLabelTile * kSmList);
     launch_softmax(dtype, grad, a, stream);
     return hip_status();
 }

@@ -18,7 +18,10 @@
 // D is rounded to the operands' type for the matrix cores: half a step of
 // relative error per entry, the size of the rounding of dW and dh
 // themselves; in fp16 it is held times 2^12, since probabilities of 1e-5
-// would be subnormal there.
+// would be subnormal there.  The entries of the labels themselves carry most
+// of the gradient, and with several labels per row they are p - 1 / m, often
+// at the foot of a binade where half a step is largest: what their rounding
+// leaves (k_sm_labels) is added to both gradients.  (With one label, -1 + p rounds well.)
 #include "kernels.hpp"
 #include "tile.hpp"
 
@@ -329,6 +332,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const int hl = lane >> 5, r32 = lane & 31;
+    if (GRAD && n0 == 0 && threadIdx.x == 0) a.count[mt0] = 0;
     if (m0 + kTM > a.L) {       // uniform: labels past the last one
         const int live = (int)(a.L - m0) - 128 * wm - 4 * hl;
 #pragma unroll
@@ -452,7 +456,102 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
         const float d = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -lse)) - share) * kDScale<DT>;
-        if (lane == 0) a.dz[dz_at(a, i, l - l0)] = (uint16_t)pack2<DT>(d, 0.f);
+        if (lane == 0) {
+            const uint32_t hi = pack2<DT>(d, 0.f);
+            a.dz[dz_at(a, i, l - l0)] = (uint16_t)hi;
+            if (p1 - p0 > 1) {
+                float up, none;
+                unpack2<DT>(hi, up, none);
+                if (p < a.rest_cap) a.rest[p] = d - up;
+                // the list is for the larger half: over a quarter of a step of the type at d
+                if (fabsf(d - up) <= fabsf(d) * (DT == HASTE_F16 ? 0x1p-12f : 0x1p-9f)) continue;
+                const int64_t block = (l - l0) / kTM;
+                const int32_t slot = atomicAdd(a.count + block, 1);     // the reader sorts
+                if (slot < kSmList)
+                    a.list[block * kSmList + slot] =
+                        u32x4_t{(uint32_t)p, (uint32_t)i | (uint32_t)((l - l0) % kTM) << 20, __float_as_uint(d - up), 0u};
+            }
+        }
+    }
+}
+
+// acc += sum over a block's list of (what rounding left of an entry of D) x
+// (its row of h): the entries as one more contraction index each, in the
+// order of the label lists (sorted here, so that the order in which they were
+// appended shows nowhere).  A block with more than kSmList of them goes
+// without.  On return the ring is free.
+// (mine: the thread's entries of the list, loaded ahead of the tile's product.)
+template <int TN>
+constexpr int kPerThread = kSmList / kThreads<TN>;
+template <int DT, int TN>
+__device__ __forceinline__ void add_rest(const SoftmaxArgs& a, int64_t n0, int64_t m0, int n,
+                                         u32x4_t (&mine)[kPerThread<TN>], uint16_t* const (&ring)[3],
+                                         f32x16_t (&acc)[4][2])
+{
+    constexpr int ST = kStage<TN>, NT = kThreads<TN>, PER = kPerThread<TN>;
+    const int tid = threadIdx.x, lane = tid & 63;
+    if (n == 0 || n > kSmList) return;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w & 1, wn = w >> 1;
+    uint32_t* const key = reinterpret_cast<uint32_t*>(ring[0]);
+    u32x2_t* const entry = reinterpret_cast<u32x2_t*>(ring[0] + 2 * kSmList);      // (rank | label << 20, rest)
+    uint16_t* const tA = ring[1];
+    uint16_t* const tB = ring[1] + kTM * ST;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (tid + NT * i >= n) mine[i][0] = ~0u;      // past the list: larger than any key
+        key[tid + NT * i] = mine[i][0];
+    }
+    __syncthreads();
+    int at[PER] = {};
+#pragma unroll 4
+    for (int o = 0; o < n; o += 4) {
+        const u32x4_t k = *reinterpret_cast<const u32x4_t*>(key + o);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            at[i] += (k[0] < mine[i][0]) + (k[1] < mine[i][0]) + (k[2] < mine[i][0]) + (k[3] < mine[i][0]);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (tid + NT * i < n) entry[at[i]] = u32x2_t{mine[i][1], mine[i][2]};
+    // rows of h of the entries e0 .. e0 + ST - 1, a run ahead of their products
+    constexpr int PA = ST * kTM / 8 / NT;
+    u32x4_t rows[PA];
+    auto load = [&](int e0) {
+#pragma unroll
+        for (int i = 0; i < PA; ++i) {
+            const int u = tid + NT * i, k = u / (kTM / 8), c = (u % (kTM / 8)) ^ (4 * (k & 3));
+            const int64_t j = m0 + 8 * c < a.Hp - 8 ? m0 + 8 * c : a.Hp - 8;
+            rows[i] = e0 + k < n ? ldg16(a.hc + (int64_t)(entry[e0 + k][0] & 0xfffffu) * a.Hp + j)
+                                 : u32x4_t{0u, 0u, 0u, 0u};
+        }
+    };
+    __syncthreads();
+    load(0);
+    for (int e0 = 0; e0 < n; e0 += ST) {
+#pragma unroll
+        for (int i = 0; i < PA; ++i) reinterpret_cast<u32x4_t*>(tA)[tid + NT * i] = rows[i];
+#pragma unroll
+        for (int u = tid; u < ST * TN / 8; u += NT) reinterpret_cast<u32x4_t*>(tB)[u] = u32x4_t{0u, 0u, 0u, 0u};
+        __syncthreads();
+        if (e0 + ST < n) load(e0 + ST);
+        if (tid < ST && e0 + tid < n) {
+            const u32x2_t v = entry[e0 + tid];
+            const int l = (int)(v[0] >> 20) - (int)(n0 % kTM);
+            if (l >= 0 && l < TN)
+                tB[tid * TN + 8 * ((l / 8) ^ (4 * (tid & 3))) + l % 8] = (uint16_t)pack2<DT>(__uint_as_float(v[1]), 0.f);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < ST / 16; ++s) {
+            u32x4_t af[4], bf[2];
+            fragments<TN, true, ST>(tB, 2 * wn, s, lane, bf);
+            fragments<kTM, true, ST>(tA, 4 * wm, s, lane, af);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) acc[mt][nt] = mfma32<DT>(af[mt], bf[nt], acc[mt][nt]);
+        }
+        __syncthreads();
     }
 }
 
@@ -465,8 +564,14 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
     const int nv = *a.nv;
     const Operand A{a.hc, a.Hp, a.Hp, a.Bp};
     const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
+    // the block's list, whole: what lies past its length is not used
+    const int rest = nv > 0 ? a.count[n0 / kTM] : 0;
+    u32x4_t mine[kPerThread<TN>];
+#pragma unroll
+    for (int i = 0; i < kPerThread<TN>; ++i) mine[i] = a.list[n0 / kTM * kSmList + threadIdx.x + kThreads<TN> * i];
     f32x16_t acc[4][2];
     tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage<TN> - 1) / kStage<TN>, ring, acc);
+    add_rest<DT, TN>(a, n0, m0, rest, mine, ring, acc);
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const float f = a.scale / kDScale<DT>;
     uint16_t* const dW = reinterpret_cast<uint16_t*>(a.dW);
@@ -597,6 +702,19 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
             widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * kDhRows + i) * a.Hp + j, 8), w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+        // what rounding left of the row's own entries of D
+        const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
+        if (p1 - p0 > 1) {
+            for (int p = p0 + g; p < p1 && p < a.rest_cap; p += 8) {
+                const int64_t l = a.y_col[p];
+                if (l < 0 || l >= a.L) continue;
+                const float r = a.rest[p];
+                float w[8];
+                widen8<DT>(load8<DT>(a.W, l * a.ldw + j, 8), w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += r * w[e];
+            }
         }
     }
 #pragma unroll

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "common.hpp"
+
 namespace haste {
 
 // Batch rows per dh accumulator tile (one LDS accumulator of kDhRows x H fp32
@@ -272,6 +274,10 @@ struct SoftmaxArgs {
     float* hit;             // kSmSlices x Bp: shares of the mean logit of the row's labels
     float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
     float* part;            // label tiles x Bp x (max, sum), units of log 2
+    float* rest;            // rest_cap: by place in y_col, what rounding left of the label's entry of D
+    int64_t rest_cap;
+    int32_t* count;         // blocks of 256 labels of a piece: entries appended to the block's list
+    u32x4_t* list;          // kSmList per block: (place in y_col, rank | label << 20, rest, 0)
     uint16_t* hc;           // Bp x Hp
     uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
     float* dhp;             // partials of dh, at most max(kSmDhSlots, tiles) tiles of 256 x 128
@@ -279,6 +285,8 @@ struct SoftmaxArgs {
 constexpr int64_t kSmLabelTile = 256;
 constexpr int64_t sm_row_tile(int64_t B) { return B > 128 ? 256 : 128; }
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
+constexpr int64_t kSmRest = 64;        // places of y_col per row that are corrected for rounding, on average
+constexpr int kSmList = 512;           // and entries per block of 256 labels
 constexpr int kSmSlices = 4;           // workgroups that share a row's labels
 void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s);
 
