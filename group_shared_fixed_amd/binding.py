@@ -646,6 +646,10 @@ def order_slots(idx, W=None, G=None, perm=False, stream=None):
 
 # ------------------------------------------------ norm, dropout, scoring, softmax loss
 
+# These calls are small next to Python's own costs on single rows, so their
+# marshalling avoids what it can: pointers go as plain integers, the stream
+# comes from torch's raw getter, and checks read each property once.
+
 _DTYPES = None
 
 
@@ -661,18 +665,27 @@ def _dtype_code(t):
     return code
 
 
+def _matrix(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be two-dimensional, got {tuple(t.shape)}")
+    return t.shape
+
+
 def _ld(t, shape, dtype, what):
     """Row stride (elements) of a 2-D tensor whose rows are contiguous."""
-    if t.shape != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise ValueError(f"{what} must be {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    ld = t.stride(0)
-    if (t.stride(1) != 1 and shape[1] > 1) or (ld < shape[1] and shape[0] > 1):
+    rows, cols = shape
+    if t.is_contiguous():
+        return cols
+    ld, one = t.stride()
+    if (one != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{what} must have contiguous rows, no two overlapping")
-    return ld if shape[0] > 1 else max(ld, shape[1])
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _dense(t, shape, dtype, what):
-    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous()):
         raise ValueError(f"{what} must be contiguous {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     return t
 
@@ -685,12 +698,27 @@ def _codes(t, what):
     return t
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _together(x, *others):
     """Every tensor of a call on one device (a host pointer in a kernel would fault)."""
-    d = x.device
+    d = x.get_device()
     for t in others:
-        if t is not None and t.device != d:
-            raise ValueError(f"all tensors of a call must be on one device, got {d} and {t.device}")
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"all tensors of a call must be on one device, got {x.device} and {t.device}")
+
+
+def _on(t, stream):
+    """hipStream_t of the call: the given stream, or torch's current one on the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()
+    d = t.get_device()
+    if d < 0:
+        raise ValueError("tensors must be on the GPU")
+    return torch._C._cuda_getCurrentRawStream(d)
 
 
 _MASK64 = (1 << 64) - 1
@@ -701,19 +729,18 @@ def dropout(x, p, seed, offset=0, residual=None, out=None, offset_dev=None, stre
     gradient of x is dropout(dy, p, seed, offset).  offset_dev: int64 tensor of one element added to
     offset when the call runs (for captured graphs)."""
     torch = _torch()
-    if x.dim() != 2:
-        raise ValueError("x must be rows x cols")
-    code, (rows, cols) = _dtype_code(x), x.shape
-    ldx = _ld(x, x.shape, x.dtype, "x")
-    ldr = _ld(residual, x.shape, x.dtype, "residual") if residual is not None else 0
+    code, shape = _dtype_code(x), _matrix(x, "x")
+    rows, cols = shape
+    ldx = _ld(x, shape, x.dtype, "x")
+    ldr = _ld(residual, shape, x.dtype, "residual") if residual is not None else 0
     if out is None:
         out = torch.empty(rows, cols, dtype=x.dtype, device=x.device)
     else:
-        _dense(out, x.shape, x.dtype, "out")
+        _dense(out, shape, x.dtype, "out")
     _together(x, residual, out, offset_dev)
     _check("haste_dropout", lib().haste_dropout(
-        _ptr(x), _ptr(residual), _ptr(out), rows, cols, ldx, ldr, float(p), seed & _MASK64, offset & _MASK64,
-        _ptr(offset_dev), code, _stream(x, stream)))
+        _at(x), _at(residual), _at(out), rows, cols, ldx, ldr, float(p), seed & _MASK64, offset & _MASK64,
+        _at(offset_dev), code, _on(x, stream)))
     return out
 
 
@@ -722,11 +749,10 @@ def add_norm(x, gamma, residual=None, eps=1e-6, p=0.0, seed=0, offset=0, want_y=
     """v = residual + dropout(x); y = v / sqrt(mean v^2 + eps) gamma per row.  Returns dict(sum = v, and
     y and rstd with want_y, and q (E4M3) and scale (one per row) with want_a8)."""
     torch = _torch()
-    if x.dim() != 2:
-        raise ValueError("x must be rows x cols")
-    code, (rows, cols) = _dtype_code(x), x.shape
-    ldx = _ld(x, x.shape, x.dtype, "x")
-    ldr = _ld(residual, x.shape, x.dtype, "residual") if residual is not None else 0
+    code, shape = _dtype_code(x), _matrix(x, "x")
+    rows, cols = shape
+    ldx = _ld(x, shape, x.dtype, "x")
+    ldr = _ld(residual, shape, x.dtype, "residual") if residual is not None else 0
     _dense(gamma, (cols,), x.dtype, "gamma")
     if out is None:
         out = {"sum": torch.empty(rows, cols, dtype=x.dtype, device=x.device)}
@@ -738,16 +764,16 @@ def add_norm(x, gamma, residual=None, eps=1e-6, p=0.0, seed=0, offset=0, want_y=
             out["scale"] = torch.empty(rows, dtype=torch.float32, device=x.device)
     else:
         for k in ("sum", "y"):
-            _dense(out.get(k), x.shape, x.dtype, k)
+            _dense(out.get(k), shape, x.dtype, k)
         for k in ("rstd", "scale"):
             _dense(out.get(k), (rows,), torch.float32, k)
         if out.get("q") is not None and _codes(out["q"], "q").shape != x.shape:
             raise ValueError("q must have x's shape")
     _together(x, gamma, residual, offset_dev, *out.values())
     _check("haste_add_norm", lib().haste_add_norm(
-        _ptr(x), _ptr(residual), _ptr(gamma), _ptr(out.get("sum")), _ptr(out.get("y")), _ptr(out.get("q")),
-        _ptr(out.get("scale")), _ptr(out.get("rstd")), rows, cols, ldx, ldr, float(eps), float(p), seed & _MASK64,
-        offset & _MASK64, _ptr(offset_dev), code, _stream(x, stream)))
+        _at(x), _at(residual), _at(gamma), _at(out.get("sum")), _at(out.get("y")), _at(out.get("q")),
+        _at(out.get("scale")), _at(out.get("rstd")), rows, cols, ldx, ldr, float(eps), float(p), seed & _MASK64,
+        offset & _MASK64, _at(offset_dev), code, _on(x, stream)))
     return out
 
 
@@ -760,12 +786,11 @@ def add_norm_bwd(dy, sum, gamma, rstd, dsum=None, p=0.0, seed=0, offset=0, out=N
     """Backward of add_norm from dy and the forward's sum and rstd; dsum: the gradient reaching `sum` from
     later layers.  Returns dict(dres, dgamma, and dx when p > 0; without dropout dx is dres)."""
     torch = _torch()
-    if dy.dim() != 2:
-        raise ValueError("dy must be rows x cols")
-    code, (rows, cols) = _dtype_code(dy), dy.shape
-    lddy = _ld(dy, dy.shape, dy.dtype, "dy")
-    ldds = _ld(dsum, dy.shape, dy.dtype, "dsum") if dsum is not None else 0
-    _dense(sum, dy.shape, dy.dtype, "sum")
+    code, shape = _dtype_code(dy), _matrix(dy, "dy")
+    rows, cols = shape
+    lddy = _ld(dy, shape, dy.dtype, "dy")
+    ldds = _ld(dsum, shape, dy.dtype, "dsum") if dsum is not None else 0
+    _dense(sum, shape, dy.dtype, "sum")
     _dense(gamma, (cols,), dy.dtype, "gamma")
     _dense(rstd, (rows,), torch.float32, "rstd")
     if out is None:
@@ -775,26 +800,25 @@ def add_norm_bwd(dy, sum, gamma, rstd, dsum=None, p=0.0, seed=0, offset=0, out=N
             out["dx"] = torch.empty(rows, cols, dtype=dy.dtype, device=dy.device)
     else:
         for k in ("dres", "dx"):
-            _dense(out.get(k), dy.shape, dy.dtype, k)
+            _dense(out.get(k), shape, dy.dtype, k)
         _dense(out.get("dgamma"), (cols,), torch.float32, "dgamma")
     ws = workspace
     if ws is None and out.get("dgamma") is not None:
         ws = torch.empty(add_norm_workspace_size(rows, cols), dtype=torch.uint8, device=dy.device)
     _together(dy, sum, gamma, rstd, dsum, offset_dev, ws, *out.values())
     _check("haste_add_norm_bwd", lib().haste_add_norm_bwd(
-        _ptr(dy), _ptr(sum), _ptr(gamma), _ptr(rstd), _ptr(dsum), _ptr(out["dres"]), _ptr(out.get("dx")),
-        _ptr(out.get("dgamma")), rows, cols, lddy, ldds, float(p), seed & _MASK64, offset & _MASK64,
-        _ptr(offset_dev), code, _ptr(ws), ws.numel() if ws is not None else 0, _stream(dy, stream)))
+        _at(dy), _at(sum), _at(gamma), _at(rstd), _at(dsum), _at(out["dres"]), _at(out.get("dx")),
+        _at(out.get("dgamma")), rows, cols, lddy, ldds, float(p), seed & _MASK64, offset & _MASK64,
+        _at(offset_dev), code, _at(ws), ws.numel() if ws is not None else 0, _on(dy, stream)))
     return out
 
 
 def quantize_rows(x, q=None, scale=None, stream=None):
     """E4M3 codes of x with one scale per row (max |x| / 448).  Returns (q, scale)."""
     torch = _torch()
-    if x.dim() != 2:
-        raise ValueError("x must be rows x cols")
-    code, (rows, cols) = _dtype_code(x), x.shape
-    ldx = _ld(x, x.shape, x.dtype, "x")
+    code, shape = _dtype_code(x), _matrix(x, "x")
+    rows, cols = shape
+    ldx = _ld(x, shape, x.dtype, "x")
     if q is None:
         q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
     elif _codes(q, "q").shape != x.shape:
@@ -804,8 +828,8 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     else:
         _dense(scale, (rows,), torch.float32, "scale")
     _together(x, q, scale)
-    _check("haste_quantize_rows", lib().haste_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), rows, cols, ldx, code,
-                                                             _stream(x, stream)))
+    _check("haste_quantize_rows", lib().haste_quantize_rows(_at(x), _at(q), _at(scale), rows, cols, ldx, code,
+                                                             _on(x, stream)))
     return q, scale
 
 
@@ -823,8 +847,8 @@ def score_a8w8(hq, h_scale, Wq, w_scale, Z=None, stream=None):
     else:
         _dense(Z, (B, L), torch.float32, "Z")
     _together(hq, h_scale, Wq, w_scale, Z)
-    _check("haste_score_a8w8", lib().haste_score_a8w8(_ptr(hq), _ptr(h_scale), _ptr(Wq), _ptr(w_scale), _ptr(Z),
-                                                       B, H, L, _stream(hq, stream)))
+    _check("haste_score_a8w8", lib().haste_score_a8w8(_at(hq), _at(h_scale), _at(Wq), _at(w_scale), _at(Z),
+                                                       B, H, L, _on(hq, stream)))
     return Z
 
 
@@ -863,12 +887,12 @@ def _softmax(grad, h, W, y_rowptr, y_col, scale, out, workspace, stream):
     _together(h, W, y_rowptr, y_col, ws, *out.values())
     # a batch of padding alone has no label ids to point at, and reads none
     col = y_col if y_col.numel() else y_rowptr
-    head = (_ptr(h), _ptr(W), _ptr(y_rowptr), _ptr(col), float(scale))
-    stat = (_ptr(out["row_loss"]), _ptr(out["lse"]), _ptr(out["loss"]))
-    tail = (B, H, L, ldh, ldw, code, _ptr(ws), ws.numel(), _stream(h, stream))
+    head = (_at(h), _at(W), _at(y_rowptr), _at(col), float(scale))
+    stat = (_at(out["row_loss"]), _at(out["lse"]), _at(out["loss"]))
+    tail = (B, H, L, ldh, ldw, code, _at(ws), ws.numel(), _on(h, stream))
     if grad:
         _check("haste_softmax_step",
-               lib().haste_softmax_step(*head, _ptr(out["dW"]), _ptr(out["dh"]), *stat, *tail))
+               lib().haste_softmax_step(*head, _at(out["dW"]), _at(out["dh"]), *stat, *tail))
     else:
         _check("haste_softmax_loss", lib().haste_softmax_loss(*head, *stat, *tail))
     return out
