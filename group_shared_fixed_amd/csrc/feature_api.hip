@@ -51,7 +51,7 @@ struct SoftmaxLayout {
     size_t nv, rows, rank, hit, clse, part, rest, hc, dhp, dz;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
     {
-        tn = sm_row_tile(B);
+        tn = sm_row_tile(B, H, L);
         Bp = round_up(B, tn);
         Hp = round_up(H, 64);
         Lr = round_up(L, kSmLabelTile);

@@ -23,7 +23,7 @@ template <int T, bool MAX>
 __device__ __forceinline__ float row_reduce(float v, float* sh)
 {
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
+    for (int o = T < 64 ? T / 2 : 32; o >= 1; o >>= 1) {
         const float u = __shfl_xor(v, o, 64);
         v = MAX ? fmaxf(v, u) : v + u;
     }
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
     __shared__ float sh[16];
     const int t = T < 256 ? (int)threadIdx.x % T : (int)threadIdx.x;
     const int64_t row = (int64_t)blockIdx.x * RPB + (T < 256 ? threadIdx.x / T : 0);
-    if (row >= a.rows) return;                // whole waves; T > 64 has one row per workgroup
+    if (row >= a.rows) return;                // rows do not share threads; T > 64 has one row per workgroup
     const int64_t per = (a.cols + 7) / 8;
 
     Raw8<DT> rx[NV], rr[NV], rg[NV];
@@ -263,13 +263,15 @@ __global__ __launch_bounds__(256) void k_column_sum(const float* part, int64_t n
     }
 }
 
-// Threads per row: one wave up to 1024 columns (no barriers, four rows per
-// workgroup), 256 up to 8192, 1024 beyond.
+// Threads per row: a quarter or half of a wave up to 128 or 256 columns, one
+// wave up to 1024 (no barriers), 256 up to 8192, 1024 beyond.
 template <typename F>
 void by_width(int64_t cols, F&& f)
 {
     const int64_t per = (cols + 7) / 8;
-    if (per <= 64) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    if (per <= 16) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    else if (per <= 32) f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
+    else if (per <= 64) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
     else if (per <= 128) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
     else if (per <= 256) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
     else if (per <= 512) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
@@ -316,8 +318,9 @@ void launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, i
 // the dgamma partials stay small next to the rows themselves.
 int64_t norm_bwd_groups(int64_t rows, int64_t cols)
 {
-    const int64_t want = cols <= 1024 ? (rows + 3) / 4 : rows;
-    return want < 1024 ? want : 1024;
+    const int64_t per = cols <= 128 ? 16 : cols <= 256 ? 8 : cols <= 1024 ? 4 : 1;      // rows per workgroup
+    const int64_t want = (rows + per - 1) / per, most = cols <= 1024 ? 1024 : 512;
+    return want < most ? want : most;
 }
 
 void launch_add_norm_bwd(int dtype, const NormBwdArgs& a, const Drop& d, hipStream_t s)

@@ -463,10 +463,16 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
                 float up, none;
                 unpack2<DT>(hi, up, none);
                 if (p < a.rest_cap) a.rest[p] = d - up;
-                // the list is for the larger half: over a quarter of a step of the type at d
+                // the list is for the larger half: over a quarter of a step of the type at d.
+                // (With more rows than labels the blocks' lists would overflow, and the waves queue for
+                // their counters: 417 rows of 36 of 217 labels, 48 us instead of 6.)
+                if (a.B > a.L) continue;
                 if (fabsf(d - up) <= fabsf(d) * (DT == HASTE_F16 ? 0x1p-12f : 0x1p-9f)) continue;
+                // (a list that is past its length stays so: no more atomics on its counter)
+                int32_t* const count = a.count + (l - l0) / kTM;
+                if (__hip_atomic_load(count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > kSmList) continue;
                 const int64_t block = (l - l0) / kTM;
-                const int32_t slot = atomicAdd(a.count + block, 1);     // the reader sorts
+                const int32_t slot = atomicAdd(count, 1);               // the reader sorts
                 if (slot < kSmList)
                     a.list[block * kSmList + slot] =
                         u32x4_t{(uint32_t)p, (uint32_t)i | (uint32_t)((l - l0) % kTM) << 20, __float_as_uint(d - up), 0u};
@@ -583,11 +589,9 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
         });
 }
 
-// The feature gradient has few tiles and a long contraction: it takes the
-// narrow tile at every batch, two workgroups per CU, so that the label ranges
-// its tiles are split into fill the grid evenly (100 tiles in 5 ranges at
-// 3100 live rows: 216 us a piece of 32768 labels, 257 us on the wide tile).
-constexpr int kDhRows = 128;
+// The gradients take the narrow tile at every batch: two workgroups per CU
+// fill the chip more evenly with the few tiles and long contractions they have.
+constexpr int kGradTile = 128;
 
 // Label ranges that the feature gradient of nv rows is split into: as many
 // as fill the grid once, in whole blocks of D.
@@ -637,31 +641,17 @@ __device__ __forceinline__ void dh_tile(const SoftmaxArgs& a, int64_t l0, int64_
     }
 }
 
-template <int DT>
-__global__ __launch_bounds__(kThreads<256>, 2) void k_sm_dw(SoftmaxArgs a, int64_t l0, int64_t ncols)
-{
-    HASTE_SM_RING(256)
-    dw_tile<DT, 256>(a, l0, ncols, dealt_tile(), ring);
-}
-
-template <int DT>
-__global__ __launch_bounds__(kThreads<kDhRows>, 2) void k_sm_dh(SoftmaxArgs a, int64_t l0, int64_t ncols, int first)
-{
-    HASTE_SM_RING(kDhRows)
-    dh_tile<DT, kDhRows>(a, l0, ncols, first, dealt_tile(), ring);
-}
-
-// Both gradients of a piece in one launch, for batches of one row tile: the
-// products are short there, dW is bound by its stores and dh by its reads of
-// W, and run together they share the memory's time.  Workgroups
-// [0, dh_grid) take dh.
+// Both gradients of a piece in one launch: dW has its stores where dh has its
+// reads of W, and together their last tiles share the chip (4096 x 32768 x 768:
+// 434 us, 488 one after the other on the tiles that are best for each).
+// Workgroups [0, dh_grid) take dh.
 template <int DT>
 __global__ __launch_bounds__(256, 2) void k_sm_grads(SoftmaxArgs a, int64_t l0, int64_t ncols, int first,
                                                      uint32_t dh_grid)
 {
-    HASTE_SM_RING(128)
-    if (blockIdx.x < dh_grid) dh_tile<DT, 128>(a, l0, ncols, first, dealt_tile(blockIdx.x, dh_grid), ring);
-    else dw_tile<DT, 128>(a, l0, ncols, dealt_tile(blockIdx.x - dh_grid, gridDim.x - dh_grid), ring);
+    HASTE_SM_RING(kGradTile)
+    if (blockIdx.x < dh_grid) dh_tile<DT, kGradTile>(a, l0, ncols, first, dealt_tile(blockIdx.x, dh_grid), ring);
+    else dw_tile<DT, kGradTile>(a, l0, ncols, dealt_tile(blockIdx.x - dh_grid, gridDim.x - dh_grid), ring);
 }
 
 // dh by row from the partials (0 for rows without labels); workgroup 0 also
@@ -687,7 +677,7 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
     __shared__ float part[8][32][9];
     const int64_t per = a.H / 8, n = a.B * per;
     const float f = a.scale / kDScale<DT>;
-    const int64_t nvt = (*a.nv + kDhRows - 1) / kDhRows;
+    const int64_t nvt = (*a.nv + kGradTile - 1) / kGradTile;
     const int64_t splits = nvt ? dh_splits(a, ncols * nvt) : 0;
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const int64_t t = (int64_t)(blockIdx.x - 1) * 32 + c;
@@ -699,7 +689,7 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
 #pragma unroll 4
         for (int64_t s = g; s < splits; s += 8) {
             float w[8];
-            widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * kDhRows + i) * a.Hp + j, 8), w);
+            widen8<HASTE_F32>(load8<HASTE_F32>(a.dhp, (s * nvt * kGradTile + i) * a.Hp + j, 8), w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
@@ -746,19 +736,14 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
     k_sm_logits<DT, TN, false><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0);
     k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
     if (grad) {
-        const int64_t dh_tiles = ncols * (a.Bp / kDhRows), dh_grid = ((dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots) + 7) / 8 * 8;
+        const int64_t dh_tiles = ncols * (a.Bp / kGradTile), dh_grid = ((dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots) + 7) / 8 * 8;
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
             k_sm_logits<DT, TN, true><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
-            const int64_t dw_tiles = (live + TN - 1) / TN * ncols;
-            if constexpr (TN == 256) {
-                k_sm_dw<DT><<<(unsigned)dw_tiles, NT, 0, s>>>(a, l0, ncols);
-                k_sm_dh<DT><<<(unsigned)dh_grid, kThreads<kDhRows>, 0, s>>>(a, l0, ncols, l0 == 0);
-            } else {
-                k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), NT, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);
-            }
+            const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols;
+            k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);
         }
     }
     const int64_t blocks = grad ? (a.B * (a.H / 8) + 31) / 32 : 0;
