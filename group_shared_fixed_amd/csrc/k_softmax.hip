@@ -310,12 +310,27 @@ __device__ __forceinline__ void store_tile(uint16_t* const (&ring)[3], Value&& v
     else store_rows<DT>(ring[1], lane, value, put);
 }
 
+// What the caller sees of rank n, and its log2-sum-exp for the passes after.
+__device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, float lse2)
+{
+    float hit = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSmSlices; ++k) hit += a.hit[k * a.Bp + n];
+    const float lse = lse2 * kLn2;
+    const int64_t b = a.rows[n];
+    a.clse[n] = lse2;
+    a.lse[b] = lse;
+    a.row_loss[b] = lse - hit;
+}
+
 // Logits of one 256-label x TN-row tile, in units of log 2 from the
-// exponential on: GRAD = false: the tile's (maximum, sum of powers of two)
-// per row.  GRAD = true: D = softmax of the piece of labels [l0, l0 + Lc),
-// without the labels' own terms.
-template <int DT, int TN, bool GRAD>
-__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0)
+// exponential on.  PASS = kStatistics: the tile's (maximum, sum of powers of
+// two) per row.  kGradient: D = softmax of the piece of labels [l0, l0 + Lc),
+// without the labels' own terms.  kOneTile, for label spaces of one tile: the
+// rows' results and (grad) D at once, with no second pass and no k_sm_lse.
+enum Pass { kStatistics, kGradient, kOneTile };
+template <int DT, int TN, Pass PASS>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0, bool grad)
 {
     HASTE_SM_RING(TN)
     __shared__ float red[2][TN][2];
@@ -324,6 +339,10 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
     const int64_t first = t / (8 * nrt) * 8, loc = t % (8 * nrt), gl = nlt - first < 8 ? nlt - first : 8;
     const int64_t mt0 = first + loc % gl, n0 = loc / gl * TN;
     const int nv = *a.nv;
+    if (PASS == kOneTile && threadIdx.x < TN) {
+        const int64_t b = n0 + threadIdx.x;
+        if (b < a.B && a.rank[b] < 0) a.lse[b] = a.row_loss[b] = 0.f;
+    }
     if (n0 >= nv) return;
     const int64_t m0 = l0 + mt0 * kTM;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
@@ -332,7 +351,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 
     const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const int hl = lane >> 5, r32 = lane & 31;
-    if (GRAD && n0 == 0 && threadIdx.x == 0) a.count[mt0] = 0;
+    if (grad && n0 == 0 && threadIdx.x == 0) a.count[mt0] = 0;
     if (m0 + kTM > a.L) {       // uniform: labels past the last one
         const int live = (int)(a.L - m0) - 128 * wm - 4 * hl;
 #pragma unroll
@@ -341,18 +360,13 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
             for (int e = 0; e < 16; ++e)
                 if (32 * mt + 8 * (e >> 2) + (e & 3) >= live) acc[mt][0][e] = acc[mt][1][e] = -INFINITY;
     }
-    if constexpr (GRAD) {
-        float off[2];
+    float off[2];              // exponent of D over z log2 e, per row
+    if constexpr (PASS == kGradient) {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
             const int64_t n = n0 + 64 * wn + 32 * nt + r32;
             off[nt] = n < nv ? kDLog2<DT> - a.clse[n] : -INFINITY;
         }
-        uint16_t* const dst = a.dz + dz_at(a, n0 + 64 * wn, mt0 * kTM + 128 * wm);
-        store_tile<DT, TN>(
-            ring,
-            [&](int mt, int nt, int e) { return __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, off[nt])); },
-            [&](int r, int c, u32x4_t v) { *reinterpret_cast<u32x4_t*>(dst + r * kTM + 8 * c) = v; });
     } else {
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
@@ -382,8 +396,29 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
             const float top = fmaxf(t0, t1), base = top == -INFINITY ? 0.f : top;
             const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f(t0 - base) +
                               red[1][threadIdx.x][1] * __builtin_amdgcn_exp2f(t1 - base);
-            *reinterpret_cast<f32x2_t*>(a.part + 2 * (mt0 * a.Bp + n0 + threadIdx.x)) = f32x2_t{top, sum};
+            const int64_t n = n0 + threadIdx.x;
+            if constexpr (PASS == kStatistics) {
+                *reinterpret_cast<f32x2_t*>(a.part + 2 * (mt0 * a.Bp + n)) = f32x2_t{top, sum};
+            } else {
+                float lse2 = INFINITY;
+                if (n < nv) {
+                    lse2 = base + log2f(sum);
+                    row_results(a, n, lse2);
+                }
+                red[0][threadIdx.x][0] = lse2;
+            }
         }
+        if (PASS == kStatistics || !grad) return;
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) off[nt] = kDLog2<DT> - red[0][64 * wn + 32 * nt + r32][0];
+    }
+    if constexpr (PASS != kStatistics) {
+        uint16_t* const dst = a.dz + dz_at(a, n0 + 64 * wn, mt0 * kTM + 128 * wm);
+        store_tile<DT, TN>(
+            ring,
+            [&](int mt, int nt, int e) { return __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, off[nt])); },
+            [&](int r, int c, u32x4_t v) { *reinterpret_cast<u32x4_t*>(dst + r * kTM + 8 * c) = v; });
     }
 }
 
@@ -425,13 +460,7 @@ __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
         sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 32; ++k) sum += ss[k][c] * __builtin_amdgcn_exp2f(st[k][c] - base);
-        const float lse2 = base + log2f(sum), lse = lse2 * kLn2;
-        float hit = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSmSlices; ++k) hit += a.hit[k * a.Bp + i];
-        a.clse[i] = lse2;
-        a.lse[a.rows[i]] = lse;
-        a.row_loss[a.rows[i]] = lse - hit;
+        row_results(a, i, base + log2f(sum));
     }
     // rows without labels
     if (threadIdx.x < 8) {
@@ -733,14 +762,19 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
         k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
         k_sm_gather<DT, false><<<by_rank, 256, 0, s>>>(a);
     }
-    k_sm_logits<DT, TN, false><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0);
-    k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
+    const bool one = tiles == 1;
+    if (one) {
+        k_sm_logits<DT, TN, kOneTile><<<(unsigned)nrt, NT, 0, s>>>(a, 0, grad);
+    } else {
+        k_sm_logits<DT, TN, kStatistics><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
+        k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
+    }
     if (grad) {
         const int64_t dh_tiles = ncols * (a.Bp / kGradTile), dh_grid = ((dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots) + 7) / 8 * 8;
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
-            k_sm_logits<DT, TN, true><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0);
+            if (!one) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
             const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols;
             k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);
