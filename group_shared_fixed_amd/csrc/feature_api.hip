@@ -67,9 +67,11 @@ struct SoftmaxLayout {
         nv = take(4);
         rows = take((size_t)Bp * 4);
         rank = take((size_t)B * 4);
-        hit = take((size_t)Bp * 4 * kSmSlices);
+        hit = take((size_t)Bp * 4 * (size_t)sm_slices(B));
         clse = take((size_t)Bp * 4);
-        part = take((size_t)(Lr / kSmLabelTile) * (size_t)Bp * 8);
+        // a pair per row and label tile, or workgroup of the streaming kernels
+        const int64_t parts = Lr / kSmLabelTile;
+        part = take((size_t)(parts > kSmNarrowSlots ? parts : kSmNarrowSlots) * (size_t)Bp * 8);
         rest = grad ? take((size_t)(Bp * kSmRest) * 4) : at;
         hc = take((size_t)Bp * (size_t)Hp * 2);
         dhp = grad ? take((size_t)(tiles > kSmDhSlots ? tiles : kSmDhSlots) * (size_t)(128 * kSmLabelTile) * 4) : at;
@@ -116,7 +118,7 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.h = h; a.W = W; a.y_rowptr = y_rowptr; a.y_col = y_col;
     a.B = B; a.H = H; a.L = L; a.ldh = ldh; a.ldw = ldw; a.scale = scale;
     a.dW = dW; a.dh = dh; a.row_loss = row_loss; a.lse = lse; a.loss = loss;
-    a.tn = l.tn; a.Bp = l.Bp; a.Hp = l.Hp;
+    a.tn = l.tn; a.slices = sm_slices(B); a.narrow = sm_narrow(B, H, L); a.Bp = l.Bp; a.Hp = l.Hp;
     a.Lc = l.want;
     if (grad && workspace_bytes < l.total(l.want, true))
         a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / l.block()) * kSmLabelTile);

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
     if (!live) return;
     const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
     float s = 0.f;
-    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * kSmSlices) {
+    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * (int)gridDim.y) {
         const int64_t l = a.y_col[p];
         if (l >= 0 && l < a.L) s += wave_dot<DT>(a, src, l, lane);
     }
@@ -314,8 +314,8 @@ __device__ __forceinline__ void store_tile(uint16_t* const (&ring)[3], Value&& v
 __device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, float lse2)
 {
     float hit = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSmSlices; ++k) hit += a.hit[k * a.Bp + n];
+#pragma unroll 4
+    for (int k = 0; k < a.slices; ++k) hit += a.hit[k * a.Bp + n];
     const float lse = lse2 * kLn2;
     const int64_t b = a.rows[n];
     a.clse[n] = lse2;
@@ -480,7 +480,7 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
     const int64_t b = a.rows[i];
     const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
     const float share = 1.0f / (float)(p1 - p0), lse = a.clse[i];
-    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * kSmSlices) {
+    for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * (int)gridDim.y) {
         const int64_t l = a.y_col[p];
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
@@ -607,7 +607,7 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
     f32x16_t acc[4][2];
     tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage<TN> - 1) / kStage<TN>, ring, acc);
     add_rest<DT, TN>(a, n0, m0, rest, mine, ring, acc);
-    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
+    const int wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
     const float f = a.scale / kDScale<DT>;
     uint16_t* const dW = reinterpret_cast<uint16_t*>(a.dW);
     const int64_t l = l0 + n0 + 64 * wn, j = m0 + 128 * wm;
@@ -683,6 +683,184 @@ __global__ __launch_bounds__(256, 2) void k_sm_grads(SoftmaxArgs a, int64_t l0, 
     else dw_tile<DT, kGradTile>(a, l0, ncols, dealt_tile(blockIdx.x - dh_grid, gridDim.x - dh_grid), ring);
 }
 
+// Logits of batches of up to 128 rows: the time is that of streaming W, so W
+// moves in whole label rows (stages of 16, contiguous memory), and the rows
+// of h stay in registers (wave w: rows 16 w .., all of H), so that nothing
+// else moves.  One workgroup of eight waves per CU walks a range of labels on
+// a ring of up to eight stages that stays full from the first to the last.
+// (In tiles of 256 labels x 32 columns, as the general pass takes them, the
+// stages of one label row come many microseconds apart.)
+// SW: 32-wide steps of H, a multiple of eight.  LDS image of a stage: piece p
+// of label row r at p ^ r % 16 of the row (a read of 16 rows meets 16 banks).
+// GRAD = false: the range's (maximum, sum) per row into part[workgroup]; true:
+// D (n a multiple of 256; labels past the last one get 0).
+template <int SW, bool GRAD>
+constexpr int kNarrowRing = GRAD ? (SW == 32 ? 4 : SW == 24 ? 5 : 8) : (SW == 32 ? 4 : SW == 24 ? 6 : 8);
+
+// 16x16x32 product of either 16-bit type (layout at mfma16).
+template <int DT>
+__device__ __forceinline__ f32x4_t mfma16t(u32x4_t a, u32x4_t b, f32x4_t c)
+{
+    if constexpr (DT == HASTE_BF16) return mfma16(a, b, c);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                      0, 0, 0);
+}
+
+// Operands of eight steps: p[t] is the lane's place for step t of four, the
+// next four are 256 bytes on.  The read and its wait are one asm group, since
+// the ring's buffers are picked at run time and the compiler would wait for
+// every move in flight.
+__device__ __forceinline__ void read_steps(const uint32_t (&p)[4], int base, u32x4_t (&f)[8])
+{
+    asm volatile("ds_read_b128 %0, %8\n\t"
+                 "ds_read_b128 %1, %9\n\t"
+                 "ds_read_b128 %2, %10\n\t"
+                 "ds_read_b128 %3, %11\n\t"
+                 "ds_read_b128 %4, %8 offset:256\n\t"
+                 "ds_read_b128 %5, %9 offset:256\n\t"
+                 "ds_read_b128 %6, %10 offset:256\n\t"
+                 "ds_read_b128 %7, %11 offset:256\n\t"
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(f[0]), "=&v"(f[1]), "=&v"(f[2]), "=&v"(f[3]), "=&v"(f[4]), "=&v"(f[5]), "=&v"(f[6]),
+                   "=&v"(f[7])
+                 : "v"(p[0] + base), "v"(p[1] + base), "v"(p[2] + base), "v"(p[3] + base)
+                 : "memory");
+}
+
+template <int DT, int SW, bool GRAD>
+__global__ __launch_bounds__(512, 2) void k_sm_narrow(SoftmaxArgs a, int64_t l0, int64_t n, int64_t span)
+{
+    constexpr int R = kNarrowRing<SW, GRAD>, NM = SW / 8, BUF = 16 * 32 * SW;      // stages, moves per wave, elements
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[R * BUF];
+    __shared__ __attribute__((aligned(16))) uint16_t out[GRAD ? 8 * 1024 : 8];     // 16 rows of 64 labels per wave
+    const int nv = *a.nv;
+    const int64_t lo = (int64_t)blockIdx.x * span, hi = lo + span < n ? lo + span : n;
+    if (GRAD)
+        for (int64_t b = (int64_t)blockIdx.x * 512 + threadIdx.x; b < n / kTM; b += (int64_t)gridDim.x * 512) a.count[b] = 0;
+    if (nv == 0 || lo >= hi) return;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t lim = (hi < a.L - l0 ? hi : a.L - l0) - lo;        // labels of the range that exist
+    const int total = (int)((hi - lo + 15) / 16);
+
+    // moves: piece u = tid + 512 i of the stage is place u % (4 SW) of label row u / (4 SW)
+    const uint32_t pitch = 2 * (uint32_t)a.ldw;
+    // (a range wholly past the last label, at the end of a piece, reads that label)
+    const char* const W = reinterpret_cast<const char*>(reinterpret_cast<const uint16_t*>(a.W) +
+                                                        (lim > 0 ? l0 + lo : a.L - 1) * a.ldw);
+    uint32_t mrow[NM], mcol[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+        const uint32_t u = (uint32_t)tid + 512 * i;
+        mrow[i] = u / (4 * SW);
+        const uint32_t c = 8 * ((u % (4 * SW)) ^ mrow[i]), last = (uint32_t)a.H - 8;
+        mcol[i] = 2 * (c < last ? c : last);                         // past H: h is 0 there
+    }
+    int mg = 0, mslot = 0;
+    auto move = [&]() {
+        const int64_t rows = lim - 16 * (int64_t)mg;                 // past the last label: the last one again
+        const uint32_t last = rows >= 16 ? 15u : rows < 1 ? 0u : (uint32_t)rows - 1;
+        const char* const from = rows < 1 ? W : W + 16 * (int64_t)mg * pitch;
+        uint16_t* const buf = ring + mslot * BUF + 512 * w;
+#pragma unroll
+        for (int i = 0; i < NM; ++i)
+            move16(from + ((mrow[i] < last ? mrow[i] : last) * pitch + mcol[i]), buf + 4096 * i);
+        mslot = mslot + 1 == R ? 0 : mslot + 1;
+        if (mg + 1 < total) ++mg;                                    // past the end: the last stage again
+    };
+#pragma unroll
+    for (int r = 0; r < R - 1; ++r) move();
+
+    // the wave's rows of h; waves past the ranks that the gradients read rest
+    const bool active = 16 * w < (nv + 31) / 32 * 32;
+    u32x4_t h[SW];
+#pragma unroll
+    for (int s = 0; s < SW; ++s)
+        h[s] = active && 32 * s + 8 * q < a.Hp
+                   ? ldg16(a.hc + (int64_t)(16 * w + r16) * a.Hp + 32 * s + 8 * q) : u32x4_t{0u, 0u, 0u, 0u};
+    const float off = GRAD && 16 * w + r16 < nv ? kDLog2<DT> - a.clse[16 * w + r16] : -INFINITY;
+    float top = -INFINITY, sum = 0.f;
+    const uint32_t at = lds_address(ring) + 64 * SW * (uint32_t)r16;
+    uint32_t p[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) p[t] = at + 16 * (uint32_t)((4 * t + q) ^ r16);
+    uint16_t* const sg = out + 1024 * w;
+
+    int slot = 0;
+    for (int g = 0; g < total; ++g) {
+        wait_stage<NM*(R - 2)>();       // this wave's moves of the stage
+        stage_barrier();                // everyone's; and the stage before has been read by all
+        move();                         // into its buffer
+        const int base = 2 * slot * BUF;
+        slot = slot + 1 == R ? 0 : slot + 1;
+        if (!active) continue;          // the whole wave
+        f32x4_t acc[4] = {zero4(), zero4(), zero4(), zero4()};
+#pragma unroll
+        for (int j = 0; j < SW / 8; ++j) {
+            u32x4_t f[8];
+            read_steps(p, base + 512 * j, f);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) acc[t & 3] = mfma16t<DT>(f[t], h[8 * j + t], acc[t & 3]);
+        }
+        // lane: row 16 w + r16, labels 16 g + 4 q + i
+        f32x4_t z = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        const int64_t left = lim - 16 * (int64_t)g - 4 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i >= left) z[i] = -INFINITY;
+        if constexpr (!GRAD) {
+            const float m = fmaxf(top, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) * kLog2e);
+            const float b = m == -INFINITY ? 0.f : m;
+            sum *= __builtin_amdgcn_exp2f(top - b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += __builtin_amdgcn_exp2f(fmaf(z[i], kLog2e, -b));
+            top = m;
+        } else {
+            float d[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = __builtin_amdgcn_exp2f(fmaf(z[i], kLog2e, off));
+            // four stages, 64 labels, before they are stored: piece c of row r at c ^ r % 8
+            *reinterpret_cast<u32x2_t*>(sg + 64 * r16 + 8 * ((2 * (g & 3) + (q >> 1)) ^ (r16 & 7)) + 4 * (q & 1)) =
+                u32x2_t{pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3])};
+            if ((g & 3) == 3 || g + 1 == total) {
+                wave_sync();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 8 * i + (lane >> 3), c = lane & 7;
+                    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(sg + 64 * r + 8 * (c ^ (r & 7)));
+                    const int64_t l = lo + 64 * (int64_t)(g >> 2) + 8 * c;
+                    if (l < hi && l < lo + 16 * (int64_t)(g + 1))
+                        *reinterpret_cast<u32x4_t*>(a.dz + dz_at(a, 16 * w + r, l)) = v;
+                }
+                wave_sync();
+            }
+        }
+    }
+    wait_stage<0>();                    // no move may outlive the workgroup
+    if (!GRAD && active) {
+#pragma unroll
+        for (int o = 16; o < 64; o <<= 1) {
+            const float t1 = __shfl_xor(top, o, 64), s1 = __shfl_xor(sum, o, 64);
+            const float m = fmaxf(top, t1), b = m == -INFINITY ? 0.f : m;
+            sum = sum * __builtin_amdgcn_exp2f(top - b) + s1 * __builtin_amdgcn_exp2f(t1 - b);
+            top = m;
+        }
+        if (q == 0)
+            *reinterpret_cast<f32x2_t*>(a.part + 2 * ((int64_t)blockIdx.x * a.Bp + 16 * w + r16)) = f32x2_t{top, sum};
+    }
+}
+
+template <int DT, bool GRAD>
+void launch_narrow(const SoftmaxArgs& a, int64_t l0, int64_t n, int64_t span, hipStream_t s)
+{
+    const unsigned g = (unsigned)((n + span - 1) / span);
+    if (a.Hp <= 256) k_sm_narrow<DT, 8, GRAD><<<g, 512, 0, s>>>(a, l0, n, span);
+    else if (a.Hp <= 512) k_sm_narrow<DT, 16, GRAD><<<g, 512, 0, s>>>(a, l0, n, span);
+    else if (a.Hp <= 768) k_sm_narrow<DT, 24, GRAD><<<g, 512, 0, s>>>(a, l0, n, span);
+    else k_sm_narrow<DT, 32, GRAD><<<g, 512, 0, s>>>(a, l0, n, span);
+}
+
 // dh by row from the partials (0 for rows without labels); workgroup 0 also
 // adds up the loss, in 64 bits and a fixed order.
 template <int DT>
@@ -755,7 +933,7 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
 {
     constexpr int NT = kThreads<TN>;
     const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
-    const dim3 by_rank((unsigned)a.Bp, kSmSlices);
+    const dim3 by_rank((unsigned)a.Bp, (unsigned)a.slices);
     if (a.B <= kFewRows) {
         k_sm_gather<DT, true><<<by_rank, 256, 0, s>>>(a);
     } else {
@@ -763,7 +941,13 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
         k_sm_gather<DT, false><<<by_rank, 256, 0, s>>>(a);
     }
     const bool one = tiles == 1;
-    if (one) {
+    const bool narrow = TN == 128 && a.narrow;
+    auto span_of = [](int64_t n) { return ((n + kSmNarrowSlots - 1) / kSmNarrowSlots + 7) / 8 * 8; };
+    if (narrow) {
+        const int64_t span = span_of(a.L), wgs = (a.L + span - 1) / span;
+        launch_narrow<DT, false>(a, 0, a.L, span, s);
+        k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, wgs);
+    } else if (one) {
         k_sm_logits<DT, TN, kOneTile><<<(unsigned)nrt, NT, 0, s>>>(a, 0, grad);
     } else {
         k_sm_logits<DT, TN, kStatistics><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
@@ -774,7 +958,9 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
         for (int64_t l0 = 0; l0 < a.L; l0 += a.Lc) {
             const int64_t live = a.L - l0 < a.Lc ? a.L - l0 : a.Lc;
             const int64_t lt = (live + kTM - 1) / kTM;
-            if (!one) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
+            if (narrow) {
+                launch_narrow<DT, true>(a, l0, lt * kTM, span_of(lt * kTM), s);
+            } else if (!one) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
             const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols;
             k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);

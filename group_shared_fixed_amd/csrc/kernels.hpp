@@ -266,12 +266,14 @@ struct SoftmaxArgs {
     float* loss;            // 1
     // workspace
     int64_t tn;             // rows per tile of the logits passes: sm_row_tile
+    bool narrow;            // one row tile of 128 and a long label space: the streaming kernels
     int64_t Bp, Hp;         // B and H rounded up to tn and 64
     int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
     int32_t* nv;
     int32_t* rows;          // Bp
     int32_t* rank;          // B, -1 for rows without labels
-    float* hit;             // kSmSlices x Bp: shares of the mean logit of the row's labels
+    int slices;             // sm_slices(B)
+    float* hit;             // slices x Bp: shares of the mean logit of the row's labels
     float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
     float* part;            // label tiles x Bp x (max, sum), units of log 2
     float* rest;            // rest_cap: by place in y_col, what rounding left of the label's entry of D
@@ -291,10 +293,14 @@ constexpr int64_t sm_row_tile(int64_t B, int64_t H, int64_t L)
 {
     return B > 128 && H > 256 && ((B + 255) / 256) * ((L + 255) / 256) >= 256 ? 256 : 128;
 }
+constexpr bool sm_narrow(int64_t B, int64_t H, int64_t L) { return B <= 128 && H <= 1024 && L >= 4096; }
+constexpr int64_t kSmNarrowSlots = 256;   // workgroups of those kernels: one per CU
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
 constexpr int64_t kSmRest = 64;        // places of y_col per row that are corrected for rounding, on average
 constexpr int kSmList = 512;           // and entries per block of 256 labels
-constexpr int kSmSlices = 4;           // workgroups that share a row's labels
+// Workgroups that share a row's labels: few rows may have many each, and fill
+// the chip only that way.
+constexpr int sm_slices(int64_t B) { return B <= 256 ? 16 : 4; }
 void launch_softmax(int dtype, bool grad, const SoftmaxArgs& a, hipStream_t s);
 
 }  // namespace haste

@@ -52,6 +52,12 @@ __device__ __forceinline__ void stage_barrier()
     asm volatile("" ::: "memory");
 }
 typedef __attribute__((address_space(3))) void* lds_ptr;
+// One wave's move of 64 x 16 bytes from memory into LDS, from the lanes' src
+// to the wave's dst.
+__device__ __forceinline__ void move16(const void* src, uint16_t* dst)
+{
+    __builtin_amdgcn_global_load_lds(src, (lds_ptr)dst, 16, 0, 0);
+}
 
 // Moves of one operand tile from memory straight into LDS
 // (global_load_lds_dwordx4: a lane's 16 bytes land at the wave's LDS base +
@@ -124,7 +130,7 @@ struct Mover {
                 const uint32_t k = (uint32_t)st * ST + row[i], last = (uint32_t)depth - 8;
                 o = off[i] + 2 * (k < last ? k : last);
             }
-            __builtin_amdgcn_global_load_lds(b + o, (lds_ptr)(buf + 512 * (N * wave + i)), 16, 0, 0);
+            move16(b + o, buf + 512 * (N * wave + i));
         }
     }
 };

@@ -71,7 +71,9 @@ def check(out, want, b, grad=True):
 CASES = [  # B, H, L, m, empty
     (1, 8, 1, 1, 0), (1, 64, 300, 3, 0), (2, 768, 1000, 1, 0), (5, 200, 257, 257, 0.3), (37, 96, 73, 9, 0.1),
     (16, 64, 4096, 5, 0), (33, 72, 515, 4, 0.5), (64, 256, 2000, 8, 0.2), (128, 768, 2048, 32, 0),
-    (130, 264, 1001, 4, 0.4), (257, 1000, 700, 1, 0.6), (300, 96, 513, 40, 0.95), (515, 520, 1300, 2, 0.3)]
+    (130, 264, 1001, 4, 0.4), (257, 1000, 700, 1, 0.6), (300, 96, 513, 40, 0.95), (515, 520, 1300, 2, 0.3),
+    # one row tile over a long label space: ranges of the streaming kernels that end inside tiles, pieces and the last label
+    (1, 1032, 4097, 1, 0), (20, 264, 5003, 4, 0.2), (128, 768, 4500, 30, 0), (97, 1000, 20011, 2, 0.4), (128, 64, 70001, 1, 0.1)]
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp16"])
