@@ -262,3 +262,32 @@ def test_score_nan_code_stays_in_its_row_and_label():
     nan = np.zeros((B, L), bool)
     nan[3] = nan[:, 65] = True
     assert np.array_equal(np.isnan(Z), nan) and (Z[~nan] == 64).all()
+
+
+def test_dropout_and_norm_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows, against the oracle's rows at those positions."""
+    rows, cols, p, tail = 70_000, 32_768, 0.25, 3
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device=dev())
+    y = hs.dropout(x, p, SEED, OFFSET)
+    per, first = cols // 8, (rows - tail) * (cols // 8)
+    i = np.arange(first, rows * per, dtype=np.uint64)
+    w = F.philox4x32([i % np.uint64(2**32), i >> np.uint64(32), np.full_like(i, OFFSET % 2**32),
+                      np.full_like(i, OFFSET >> 32)], [SEED % 2**32, SEED >> 32])
+    half = np.stack([h for v in w for h in (v & np.uint64(0xFFFF), v >> np.uint64(16))], 1).reshape(tail, cols)
+    assert np.array_equal(host(y[-tail:] != 0), (half >= round(p * 65536)).astype(float))
+    del y
+    x[-tail:] = torch.arange(cols, device=dev()).bfloat16() / cols
+    out = hs.add_norm(x, torch.ones(cols, dtype=torch.bfloat16, device=dev()), out={"y": torch.empty_like(x)})
+    v = host(x[-1:])
+    want = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6)
+    within(out["y"][-1:], want, u("bf16") * np.abs(want) * 1.01 + 80 * U * np.abs(want), "last row")
+
+
+def test_score_past_32_bit_offsets():
+    B, H, L = 1100, 32, 2_000_000         # Z has 2.2e9 elements
+    g = torch.Generator(device=dev()).manual_seed(3)
+    hq = torch.randn(B, H, device=dev(), generator=g).to(torch.float8_e4m3fn)
+    Wq = torch.randn(L, H, device=dev(), generator=g).to(torch.float8_e4m3fn)
+    Z = hs.score_a8w8(hq, torch.ones(B, device=dev()), Wq, torch.ones(L, device=dev()))
+    a, b = host(hq.float()[-2:]), host(Wq.float()[-300:])
+    within(Z[-2:, -300:], a @ b.T, (H + 4) * U * (np.abs(a) @ np.abs(b).T), "the last corner")

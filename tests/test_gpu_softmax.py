@@ -182,3 +182,30 @@ def test_autograd_graph_of_the_same_leaves_alive():
     assert abs(float(out["loss"][0]) - float(loss)) < 1e-5 * abs(float(loss))
     for got, ref in ((out["dh"], hf.grad), (out["dW"], Wf.grad)):
         assert float((got.float() - ref).norm() / ref.norm()) < 2 * u("bf16")
+
+
+@pytest.mark.parametrize("B", [3, 200])
+def test_past_32_bit_offsets(B):
+    """L x H past 2^31 elements: the last labels, one of them a row's own."""
+    H, L, scale = 1024, 2_200_000, 4.0
+    g = torch.Generator(device=dev()).manual_seed(4)
+    W = torch.empty(L, H, dtype=torch.bfloat16, device=dev())
+    for at in range(0, L, 1 << 18):
+        n = min(1 << 18, L - at)
+        W[at:at + n] = (torch.randn(n, H, device=dev(), generator=g) * 0.06).bfloat16()
+    h = torch.randn(B, H, device=dev(), generator=g).bfloat16()
+    col = torch.arange(B, device=dev(), dtype=torch.int32) * ((L - 1) // B)
+    col[-1] = L - 1
+    out = hs.softmax_step(h, W, torch.arange(B + 1, device=dev(), dtype=torch.int32), col, scale)
+    hf, lse = h.float(), torch.full((B,), -float("inf"), dtype=torch.float64, device=dev())
+    for at in range(0, L, 1 << 18):
+        lse = torch.logaddexp(lse, torch.logsumexp((hf @ W[at:at + (1 << 18)].float().T).double(), 1))
+    dz = (H + 8) * U * float((hf.abs() @ W[-500:].float().abs().T).max()) * 1.5
+    within(out["lse"], host(lse), dz + 64 * U * 40, "lse")
+    tail = W[-500:].float().double()
+    D = torch.exp(hf.double() @ tail.T - lse[:, None])
+    D[-1, -1] -= 1
+    want = scale * host(D.T @ hf.double())
+    bound = scale * host(((dz + 64 * U * 40) * 2 + u("bf16")) * D.abs().T @ hf.double().abs()) * 1.01
+    within(out["dW"][-500:], want, bound + u("bf16") * (np.abs(want) + bound), "dW of the last labels")
+    assert torch.isfinite(out["dh"].float()).all()
