@@ -19,32 +19,59 @@ __device__ __forceinline__ void widen16(u32x4_t c, u32x4_t& lo, u32x4_t& hi)
     hi = widen_w8(u32x2_t{c[2], c[3]}, 1.0f);
 }
 
-// Few rows: one pass over the weights.  One wave per 16 x 16 tile of (labels,
-// rows), operands straight from memory.
+// Few rows, or few tiles: one wave per 16 labels x 16 RT rows, operands
+// straight from memory, U steps of 64 codes requested ahead of their
+// products.  Bound by the reading of the weights: 1 x 89088 x 768 in 14.4 us,
+// launch and all (4.8 TB/s); U = 1 took 14.7.
+template <int RT, int U>
 __global__ __launch_bounds__(256) void k_score_few(ScoreArgs a)
 {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r16 = lane & 15, q = lane >> 4;
-    const int64_t l0 = ((int64_t)blockIdx.x * 4 + w) * 16, b0 = (int64_t)blockIdx.y * 16;
+    const int64_t l0 = ((int64_t)blockIdx.x * 4 + w) * 16, b0 = (int64_t)blockIdx.y * (16 * RT);
     if (l0 >= a.L) return;
-    const int64_t l = l0 + r16 < a.L ? l0 + r16 : a.L - 1, b = b0 + r16 < a.B ? b0 + r16 : a.B - 1;
-    const uint8_t* pw = a.Wq + l * a.H;
-    const uint8_t* ph = a.hq + b * a.H;
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
-    f32x4_t acc = zero4();
-    for (int64_t k = 16 * q; k < a.H + 16 * q; k += 64) {
-        u32x4_t w0, w1, h0, h1;
-        widen16(k < a.H ? ldg16(pw + k) : zero, w0, w1);
-        widen16(k < a.H ? ldg16(ph + k) : zero, h0, h1);
-        acc = mfma16(w0, h0, acc);
-        acc = mfma16(w1, h1, acc);
+    const int64_t l = l0 + r16 < a.L ? l0 + r16 : a.L - 1;
+    const uint8_t* const pw = a.Wq + l * a.H;
+    const uint8_t* ph[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int64_t b = b0 + 16 * t + r16;
+        ph[t] = a.hq + (b < a.B ? b : a.B - 1) * a.H;
     }
-    // lane: row b0 + r16, labels l0 + 4 q + i
-    if (b0 + r16 < a.B) {
-        const float s = a.hs[b0 + r16];
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    f32x4_t acc[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[t] = zero4();
+    for (int64_t k0 = 0; k0 < a.H; k0 += 64 * U) {
+        u32x4_t cw[U], ch[U][RT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + 64 * u + 16 * q;
+            cw[u] = k < a.H ? ldg16(pw + k) : zero;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) ch[u][t] = k < a.H ? ldg16(ph[t] + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            u32x4_t w0, w1, h0, h1;
+            widen16(cw[u], w0, w1);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                widen16(ch[u][t], h0, h1);
+                acc[t] = mfma16(w0, h0, acc[t]);
+                acc[t] = mfma16(w1, h1, acc[t]);
+            }
+        }
+    }
+    // lane: rows b0 + 16 t + r16, labels l0 + 4 q + i
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int64_t b = b0 + 16 * t + r16;
+        if (b >= a.B) continue;
+        const float s = a.hs[b];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t o = l0 + 4 * q + i;
-            if (o < a.L) a.Z[(b0 + r16) * a.L + o] = acc[i] * s * a.ws[o];
+            if (o < a.L) a.Z[b * a.L + o] = acc[t][i] * s * a.ws[o];
         }
     }
 }
@@ -182,15 +209,27 @@ __global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
         }
 }
 
-// Rows up to which the weights are streamed instead of tiled.
-constexpr int64_t kScFew = 32;
+// The tiles need enough of them to fill the card, the streams one reading of
+// the weights for each 16 to 64 rows.  us, streams against tiles, H = 768 to
+// 1024: 16 x 89088 21 and 24, 24 x 8192 8 and 14, 64 x 16384 14.1 and 15.5,
+// 2048 x 512 16 and 20; the other way 48 x 30000 18 and 15, 128 x 16384 22
+// and 18, 2048 x 1024 26 and 21, 64 x 89088 63 and 26.
+bool streams(int64_t B, int64_t L) { return B <= 16 || B * L <= 1 << 20; }
+
+template <int RT, int U>
+void launch_few(const ScoreArgs& a, hipStream_t s)
+{
+    k_score_few<RT, U><<<dim3((unsigned)((a.L + 63) / 64), (unsigned)((a.B + 16 * RT - 1) / (16 * RT))), 256, 0, s>>>(a);
+}
 
 }  // namespace
 
 void launch_score(const ScoreArgs& a, hipStream_t s)
 {
-    if (a.B <= kScFew) {
-        k_score_few<<<dim3((unsigned)((a.L + 63) / 64), (unsigned)((a.B + 15) / 16)), 256, 0, s>>>(a);
+    if (streams(a.B, a.L)) {
+        if (a.B <= 16) launch_few<1, 4>(a, s);
+        else if (a.B <= 32) launch_few<2, 2>(a, s);
+        else launch_few<4, 2>(a, s);
         return;
     }
     const int64_t tiles = (a.B + kScRows - 1) / kScRows * ((a.L + kScLabels - 1) / kScLabels);
