@@ -134,6 +134,17 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int64_t n, const floa
     }
 }
 
+// Scale of a row of E4M3 codes from its largest magnitude, and the factor that
+// makes the codes.  The scale stays a normal number: under 448 x 2^-126 the
+// quotient would be subnormal and the factor infinite.
+__device__ __forceinline__ float row_scale(float top, float& inv)
+{
+    const float s = top / 448.0f;
+    const bool tiny = s < 0x1p-126f;
+    inv = top > 0.f ? (tiny ? 0x1p126f : 448.0f / top) : 0.f;
+    return tiny && top > 0.f ? 0x1p-126f : s;
+}
+
 // v * inv as E4M3 codes (rounded to nearest even from fp32), into bytes
 // i .. i + min(8, n) - 1 of q.
 __device__ __forceinline__ void store_e4m3(uint8_t* q, int64_t i, int64_t n, const float (&v)[8], float inv)

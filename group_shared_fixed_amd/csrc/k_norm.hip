@@ -100,8 +100,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
     }
     if (a.q) {
         top = row_reduce<T, true>(top, sh);
-        if (t == 0) a.q_scale[row] = top / 448.0f;
-        const float inv = top > 0.f ? 448.0f / top : 0.f;
+        float inv;
+        const float scale = row_scale(top, inv);
+        if (t == 0) a.q_scale[row] = scale;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t b = t + (int64_t)k * T;
@@ -133,8 +134,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_quantize_rows(const void*
         }
     }
     top = row_reduce<T, true>(top, sh);
-    if (t == 0) scale[row] = top / 448.0f;
-    const float inv = top > 0.f ? 448.0f / top : 0.f;
+    float inv;
+    const float s = row_scale(top, inv);
+    if (t == 0) scale[row] = s;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int64_t b = t + (int64_t)k * T;

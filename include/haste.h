@@ -498,8 +498,8 @@ int haste_dropout(const void* x, const void* residual, void* y, int64_t rows, in
  *   rstd = 1 / sqrt(mean v^2 + eps),  y = v rstd gamma.
  * Outputs, all but one of y and q nullable: sum = v in the input's type (the
  * residual of the next block), y in the input's type, q = OCP E4M3 codes of
- * y / q_scale with q_scale[row] = max |y| / 448 (fp32; 0 for a row of zeros,
- * whose codes are 0), rstd (fp32, for the backward pass).  The statistics and
+ * y / q_scale with q_scale[row] = max |y| / 448 (fp32, no smaller than 2^-126;
+ * 0 for a row of zeros, whose codes are 0), rstd (fp32, for the backward pass).  The statistics and
  * both outputs come from the unrounded v.  gamma: cols values of the input's
  * type.  residual is nullable; sum may be x or residual if that has
  * ld = cols.  cols <= 32768.  x and residual aligned to their element, the
@@ -523,7 +523,7 @@ int haste_add_norm_bwd(const void* dy, const void* sum, const void* gamma, const
                        void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* x (rows x cols) as E4M3 codes with one scale per row, as haste_add_norm
- * writes them: q = codes of x / scale, scale = max |x| / 448. */
+ * writes them: q = codes of x / scale, scale = max(max |x| / 448, 2^-126). */
 int haste_quantize_rows(const void* x, uint8_t* q, float* scale, int64_t rows, int64_t cols, int64_t ldx, int dtype,
                         hipStream_t stream);
 

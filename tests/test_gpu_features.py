@@ -219,10 +219,25 @@ def test_quantize_rows(rows, cols, t):
     assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_quantize_rows_of_the_smallest_numbers(t):
+    """Rows whose scale would be subnormal: the scale stops at 2^-126, and a code is off by half a step of its own
+    (2^-4 of it, or 2^-10 among the subnormal codes)."""
+    top = [-108, -116, -117, -118, -119, -120, -126]
+    x, x64 = rounded(np.random.default_rng(4).uniform(-1, 1, (len(top), 300)) * 2.0 ** np.array(top)[:, None], t)
+    q, s = hs.quantize_rows(put(x))
+    scale = host(s)
+    want = np.maximum(np.abs(x64).max(1) / 448, 2.0 ** -126)
+    within(scale, want, 4 * U * want, "scale")
+    v = x64 / scale[:, None]
+    within(host(q), v, np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10) + 6 * U * np.abs(v), "codes")
+
+
 # one request, ragged rows and labels, depths that end inside a 128-deep step, several tiles both ways
 @pytest.mark.parametrize("B,H,L", [(1, 16, 1), (1, 768, 1000), (2, 144, 17), (16, 1024, 333), (17, 768, 129),
                                    (33, 80, 515), (64, 768, 1031), (65, 640, 260), (130, 256, 1001), (300, 1040, 777),
-                                   (3, 2064, 70)])
+                                   (3, 2064, 70), (17, 144, 61_700), (130, 256, 9001), (257, 80, 4100), (1025, 64, 1100),
+                                   (40, 1040, 27_001), (600, 192, 1803), (129, 16, 8193), (2100, 320, 501)])
 def test_score(B, H, L):
     rng = np.random.default_rng(B + L)
     hq = torch.from_numpy(rng.normal(size=(B, H)) * 100).clamp(-448, 448).to(torch.float8_e4m3fn)
@@ -251,8 +266,8 @@ def test_norm_codes_feed_the_scores():
     assert np.linalg.norm(Z - want) / np.linalg.norm(want) < 2.0 ** -4
 
 
-def test_score_nan_code_stays_in_its_row_and_label():
-    B, H, L = 20, 64, 70
+@pytest.mark.parametrize("B,H,L", [(20, 64, 70), (40, 80, 90), (260, 80, 4100), (260, 64, 4102)])
+def test_score_nan_code_stays_in_its_row_and_label(B, H, L):
     hq = torch.ones(B, H).to(torch.float8_e4m3fn)
     Wq = torch.ones(L, H).to(torch.float8_e4m3fn)
     hq[3, 60] = float("nan")
@@ -261,7 +276,7 @@ def test_score_nan_code_stays_in_its_row_and_label():
     Z = host(hs.score_a8w8(put(hq), one(B), put(Wq), one(L)))
     nan = np.zeros((B, L), bool)
     nan[3] = nan[:, 65] = True
-    assert np.array_equal(np.isnan(Z), nan) and (Z[~nan] == 64).all()
+    assert np.array_equal(np.isnan(Z), nan) and (Z[~nan] == H).all()
 
 
 def test_dropout_and_norm_past_32_bit_offsets():
