@@ -81,7 +81,10 @@ __global__ __launch_bounds__(256) void k_score_few(ScoreArgs a)
 // The codes move into a ring of three LDS stages of 64 (24 KB each) as they
 // are, half the bytes of bf16, and are widened between LDS and the products.
 // A lane's 16-byte read is two operands: any assignment of contraction
-// indices to steps works as long as both sides use the same.
+// indices to steps works as long as both sides use the same.  Bound by the
+// products and by the stores of Z, which overlap only in part: 2048 x 89088 x
+// 768 306 us (916 TFLOP/s), of which the products alone are 224 and 730 MB of
+// Z at the rate of a fill 107.
 // RAGGED: H % 64 != 0; the pieces past H, which repeat the last one, are
 // zeroed on the features' side.
 constexpr int kScRows = 128, kScLabels = 256, kScStage = 32;     // stage in 16-bit units
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
     // Z leaves through LDS, 16 rows x 64 labels of a wave at a time (4 KB), so
     // that an instruction stores four runs of 256 bytes; as the accumulators
     // lie, 128 bytes of two rows per instruction, it took 424 us instead of
-    // 298 at 2048 x 89088 x 768 (the products alone take 224)
+    // 306 at 2048 x 89088 x 768
     float* const sg = reinterpret_cast<float*>(ring0) + 1024 * w;     // 16 rows x 64 labels
     float sw[2];
 #pragma unroll
