@@ -49,12 +49,17 @@ __device__ __forceinline__ int64_t dz_at(const SoftmaxArgs& a, int64_t rank, int
 }
 
 // rows / rank / nv: the ranks of the rows that have labels, in row order.
-__global__ __launch_bounds__(1024) void k_sm_rows(const int32_t* __restrict__ rowptr, int64_t B, int64_t Bp,
-                                                  int32_t* __restrict__ rows, int32_t* __restrict__ rank,
-                                                  int32_t* __restrict__ nv)
+// Also clears what the passes of `keep` count in.
+__global__ __launch_bounds__(1024) void k_sm_rows(SoftmaxArgs a)
 {
     __shared__ int32_t cnt[1024];
     const int t = threadIdx.x;
+    const int64_t B = a.B;
+    const int32_t* __restrict__ const rowptr = a.y_rowptr;
+    if (a.keep) {
+        for (int64_t i = t; i < a.Lc / kTM; i += 1024) a.own[i] = a.count[i] = 0;
+        for (int64_t i = t; i <= a.Bp / a.tn; i += 1024) a.redo[i] = 0;
+    }
     const int64_t per = (B + 1023) / 1024, b0 = t * per, b1 = b0 + per < B ? b0 + per : B;
     int n = 0;
     for (int64_t b = b0; b < b1; ++b) n += rowptr[b + 1] > rowptr[b];
@@ -69,10 +74,10 @@ __global__ __launch_bounds__(1024) void k_sm_rows(const int32_t* __restrict__ ro
     int at = cnt[t] - n;
     for (int64_t b = b0; b < b1; ++b) {
         const bool has = rowptr[b + 1] > rowptr[b];
-        rank[b] = has ? at : -1;
-        if (has) rows[at++] = (int32_t)b;
+        a.rank[b] = has ? at : -1;
+        if (has) a.rows[at++] = (int32_t)b;
     }
-    if (t == 1023) *nv = cnt[1023];
+    if (t == 1023) *a.nv = cnt[1023];
 }
 
 // Batches of up to kFewRows find their ranks in the gather itself (each of
@@ -168,7 +173,12 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
     float s = 0.f;
     for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * (int)gridDim.y) {
         const int64_t l = a.y_col[p];
-        if (l >= 0 && l < a.L) s += wave_dot<DT>(a, src, l, lane);
+        if (l < 0 || l >= a.L) continue;
+        s += wave_dot<DT>(a, src, l, lane);
+        // how many entries the block's list will have (a count past the limit may stay where it is)
+        if (a.keep && lane == 0 && a.B <= a.L &&
+            __hip_atomic_load(a.own + l / kTM, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <= kSmList)
+            atomicAdd(a.own + l / kTM, 1);
     }
     if (lane == 0) sh[w] = s;
     __syncthreads();
@@ -310,6 +320,11 @@ __device__ __forceinline__ void store_tile(uint16_t* const (&ring)[3], Value&& v
     else store_rows<DT>(ring[1], lane, value, put);
 }
 
+// Rows whose log2-sum-exp lies in here have their exponentials kept as they
+// are: none overflows bf16, nor do fp32 sums of them, the factor that makes
+// them probabilities is at most 1, and what is flushed is under 2^-126.
+constexpr float kKeepLow = 0.f, kKeepHigh = 64.f;
+
 // What the caller sees of rank n, and its log2-sum-exp for the passes after.
 __device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, float lse2)
 {
@@ -321,6 +336,11 @@ __device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, flo
     a.clse[n] = lse2;
     a.lse[b] = lse;
     a.row_loss[b] = lse - hit;
+    if (a.keep) {
+        const bool fits = lse2 >= kKeepLow && lse2 <= kKeepHigh;
+        a.ref[n] = fits ? 0.f : lse2;
+        if (!fits) a.redo[0] = a.redo[1 + n / a.tn] = 1;
+    }
 }
 
 // Logits of one 256-label x TN-row tile, in units of log 2 from the
@@ -328,22 +348,12 @@ __device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, flo
 // two) per row.  kGradient: D = softmax of the piece of labels [l0, l0 + Lc),
 // without the labels' own terms.  kOneTile, for label spaces of one tile: the
 // rows' results and (grad) D at once, with no second pass and no k_sm_lse.
-enum Pass { kStatistics, kGradient, kOneTile };
+// kKeep: as kStatistics, and the exponentials themselves stay in dz.
+enum Pass { kStatistics, kKeep, kGradient, kOneTile };
 template <int DT, int TN, Pass PASS>
-__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0, bool grad)
+__device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, int64_t mt0, int64_t n0, int nv, bool grad,
+                                            uint16_t* const (&ring)[3], float (&red)[2][TN][2])
 {
-    HASTE_SM_RING(TN)
-    __shared__ float red[2][TN][2];
-    // eight label tiles by the row tiles in turn
-    const int64_t nrt = a.Bp / TN, nlt = gridDim.x / nrt, t = dealt_tile();
-    const int64_t first = t / (8 * nrt) * 8, loc = t % (8 * nrt), gl = nlt - first < 8 ? nlt - first : 8;
-    const int64_t mt0 = first + loc % gl, n0 = loc / gl * TN;
-    const int nv = *a.nv;
-    if (PASS == kOneTile && threadIdx.x < TN) {
-        const int64_t b = n0 + threadIdx.x;
-        if (b < a.B && a.rank[b] < 0) a.lse[b] = a.row_loss[b] = 0.f;
-    }
-    if (n0 >= nv) return;
     const int64_t m0 = l0 + mt0 * kTM;
     const Operand A{reinterpret_cast<const uint16_t*>(a.W), a.ldw, a.L, a.H}, B{a.hc, a.Hp, a.Bp, a.Hp};
     f32x16_t acc[4][2];
@@ -365,7 +375,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
             const int64_t n = n0 + 64 * wn + 32 * nt + r32;
-            off[nt] = n < nv ? kDLog2<DT> - a.clse[n] : -INFINITY;
+            off[nt] = n < nv ? kDLog2<DT> - (a.keep ? a.ref : a.clse)[n] : -INFINITY;
         }
     } else {
 #pragma unroll
@@ -381,8 +391,12 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    sum[mt] += __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, -base));
+                for (int e = 0; e < 16; ++e) {
+                    const float x = __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, -base));
+                    sum[mt] += x;
+                    if (PASS == kKeep) acc[mt][nt][e] = x;
+                }
+            if (PASS == kKeep) off[nt] = n0 + 64 * wn + 32 * nt + r32 < nv ? __builtin_amdgcn_exp2f(base) : 0.f;
             float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             all += __shfl_xor(all, 32, 64);
             if (hl == 0) {
@@ -397,7 +411,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
             const float sum = red[0][threadIdx.x][1] * __builtin_amdgcn_exp2f(t0 - base) +
                               red[1][threadIdx.x][1] * __builtin_amdgcn_exp2f(t1 - base);
             const int64_t n = n0 + threadIdx.x;
-            if constexpr (PASS == kStatistics) {
+            if constexpr (PASS == kStatistics || PASS == kKeep) {
                 *reinterpret_cast<f32x2_t*>(a.part + 2 * (mt0 * a.Bp + n)) = f32x2_t{top, sum};
             } else {
                 float lse2 = INFINITY;
@@ -408,17 +422,57 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
                 red[0][threadIdx.x][0] = lse2;
             }
         }
-        if (PASS == kStatistics || !grad) return;
-        __syncthreads();
+        if (PASS == kStatistics || (PASS == kOneTile && !grad)) return;
+        if constexpr (PASS == kOneTile) {
+            __syncthreads();
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) off[nt] = kDLog2<DT> - red[0][64 * wn + 32 * nt + r32][0];
+            for (int nt = 0; nt < 2; ++nt) off[nt] = kDLog2<DT> - red[0][64 * wn + 32 * nt + r32][0];
+        }
     }
     if constexpr (PASS != kStatistics) {
         uint16_t* const dst = a.dz + dz_at(a, n0 + 64 * wn, mt0 * kTM + 128 * wm);
         store_tile<DT, TN>(
             ring,
-            [&](int mt, int nt, int e) { return __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, off[nt])); },
+            [&](int mt, int nt, int e) {
+                if (PASS == kKeep) return acc[mt][nt][e] * off[nt];
+                return __builtin_amdgcn_exp2f(fmaf(acc[mt][nt][e], kLog2e, off[nt]));
+            },
             [&](int r, int c, u32x4_t v) { *reinterpret_cast<u32x4_t*>(dst + r * kTM + 8 * c) = v; });
+    }
+}
+
+// Eight label tiles by the row tiles in turn.
+template <int DT, int TN, Pass PASS>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0, bool grad)
+{
+    HASTE_SM_RING(TN)
+    __shared__ float red[2][TN][2];
+    const int64_t nrt = a.Bp / TN, nlt = gridDim.x / nrt, t = dealt_tile();
+    const int64_t first = t / (8 * nrt) * 8, loc = t % (8 * nrt), gl = nlt - first < 8 ? nlt - first : 8;
+    const int64_t mt0 = first + loc % gl, n0 = loc / gl * TN;
+    const int nv = *a.nv;
+    if (PASS == kOneTile && threadIdx.x < TN) {
+        const int64_t b = n0 + threadIdx.x;
+        if (b < a.B && a.rank[b] < 0) a.lse[b] = a.row_loss[b] = 0.f;
+    }
+    if (n0 >= nv) return;
+    logits_tile<DT, TN, PASS>(a, l0, mt0, n0, nv, grad, ring, red);
+}
+
+// Forms the kept exponentials again, as probabilities, of rows whose logits lie
+// too far from 0 (and of the other rows of their tiles, as they were).
+template <int DT, int TN>
+__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_redo(SoftmaxArgs a)
+{
+    HASTE_SM_RING(TN)
+    __shared__ float red[2][TN][2];
+    if (!a.redo[0]) return;
+    const int64_t nrt = a.Bp / TN, tiles = a.Lc / kTM * nrt;
+    const int nv = *a.nv;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        if (!a.redo[1 + t % nrt]) continue;
+        logits_tile<DT, TN, kGradient>(a, 0, t / nrt, t % nrt * TN, nv, false, ring, red);
+        __syncthreads();
     }
 }
 
@@ -469,23 +523,67 @@ __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
     }
 }
 
+// A label's own entry d = p - 1 / m where the exponentials are kept.  It leaves
+// dz for the block's list, as one or two of its entries (its rounding and, over
+// a quarter of a step, what that leaves), so that it meets h itself in dW and
+// is exact in dh; in blocks that have too many, its place in dz takes it.
+template <int DT>
+__device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t i, int64_t l, float d, float up2)
+{
+    const int64_t block = l / kTM;
+    const int n = a.own[block];
+    uint16_t* const at = a.dz + dz_at(a, i, l);
+    float hi, none;
+    if (a.B > a.L || n > kSmList || p >= a.rest_cap) {
+        const uint32_t v = pack2<DT>(d * __builtin_amdgcn_exp2f(up2), 0.f);
+        *at = (uint16_t)v;
+        unpack2<DT>(v, hi, none);
+        if (p < a.rest_cap) a.rest[p] = d - hi * __builtin_amdgcn_exp2f(-up2);
+        return;
+    }
+    *at = 0;
+    a.rest[p] = d;
+    unpack2<DT>(pack2<DT>(d, 0.f), hi, none);
+    const bool two = 2 * n <= kSmList && fabsf(d - hi) > fabsf(d) * 0x1p-10f;
+    const int32_t slot = atomicAdd(a.count + block, two ? 2 : 1);       // the reader sorts
+    u32x4_t* const to = a.list + block * kSmList + slot;
+    const uint32_t where = (uint32_t)i | (uint32_t)(l % kTM) << 20;
+    to[0] = u32x4_t{2 * (uint32_t)p, where, __float_as_uint(hi), 0u};
+    if (two) to[1] = u32x4_t{2 * (uint32_t)p + 1, where, __float_as_uint(d - hi), 0u};
+}
+
 // The labels' own entries of D in the piece [l0, l0 + Lc): workgroups as in
 // k_sm_gather.  The logit is formed again here, in fp32.
 template <int DT>
 __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
 {
     const int64_t i = blockIdx.x;
-    if (i >= *a.nv) return;
+    const bool live = i < *a.nv;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const float lse = live ? a.clse[i] : 0.f;
+    const float up2 = a.keep && live ? lse - a.ref[i] : 0.f;     // dz is held times 2^up2
+    if (a.keep && blockIdx.y == 0) {
+        const float f = __builtin_amdgcn_exp2f(-up2);
+        for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048) {
+            float x[8];
+            widen8<DT>(load8<DT>(a.hc, i * a.Hp + j, 8), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= f;
+            store8<DT>(a.hs, i * a.Hp + j, 8, x);
+        }
+    }
+    if (!live) return;
     const int64_t b = a.rows[i];
     const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
-    const float share = 1.0f / (float)(p1 - p0), lse = a.clse[i];
+    const float share = 1.0f / (float)(p1 - p0);
     for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * (int)gridDim.y) {
         const int64_t l = a.y_col[p];
         if (l < l0 || l >= l0 + a.Lc || l >= a.L || l < 0) continue;
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
         const float d = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -lse)) - share) * kDScale<DT>;
-        if (lane == 0) {
+        if (lane == 0 && a.keep) {
+            keep_label<DT>(a, p, i, l, d, up2);
+        } else if (lane == 0) {
             const uint32_t hi = pack2<DT>(d, 0.f);
             a.dz[dz_at(a, i, l - l0)] = (uint16_t)hi;
             if (p1 - p0 > 1) {
@@ -597,7 +695,7 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
 {
     const int64_t m0 = t % ncols * kTM, n0 = t / ncols * TN;
     const int nv = *a.nv;
-    const Operand A{a.hc, a.Hp, a.Hp, a.Bp};
+    const Operand A{a.hs, a.Hp, a.Hp, a.Bp};
     const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
     // the block's list, whole: what lies past its length is not used
     const int rest = nv > 0 ? a.count[n0 / kTM] : 0;
@@ -900,9 +998,14 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
-        // what rounding left of the row's own entries of D
+        if (a.keep) {
+            const float back = __builtin_amdgcn_exp2f(a.ref[i] - a.clse[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= back;
+        }
+        // what is still missing of the row's own entries of D
         const int p0 = a.y_rowptr[b], p1 = a.y_rowptr[b + 1];
-        if (p1 - p0 > 1) {
+        if (a.keep || p1 - p0 > 1) {
             for (int p = p0 + g; p < p1 && p < a.rest_cap; p += 8) {
                 const int64_t l = a.y_col[p];
                 if (l < 0 || l >= a.L) continue;
@@ -934,10 +1037,10 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
     constexpr int NT = kThreads<TN>;
     const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
     const dim3 by_rank((unsigned)a.Bp, (unsigned)a.slices);
-    if (a.B <= kFewRows) {
+    if (a.B <= kFewRows && !a.keep) {
         k_sm_gather<DT, true><<<by_rank, 256, 0, s>>>(a);
     } else {
-        k_sm_rows<<<1, 1024, 0, s>>>(a.y_rowptr, a.B, a.Bp, a.rows, a.rank, a.nv);
+        k_sm_rows<<<1, 1024, 0, s>>>(a);
         k_sm_gather<DT, false><<<by_rank, 256, 0, s>>>(a);
     }
     const bool one = tiles == 1;
@@ -950,8 +1053,15 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
     } else if (one) {
         k_sm_logits<DT, TN, kOneTile><<<(unsigned)nrt, NT, 0, s>>>(a, 0, grad);
     } else {
-        k_sm_logits<DT, TN, kStatistics><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
+        bool kept = false;
+        if constexpr (DT == HASTE_BF16 && TN == 256) {
+            if (a.keep) k_sm_logits<DT, TN, kKeep><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
+            kept = a.keep;
+        }
+        if (!kept) k_sm_logits<DT, TN, kStatistics><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
         k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
+        if constexpr (DT == HASTE_BF16 && TN == 256)
+            if (kept) k_sm_redo<DT, TN><<<256, NT, 0, s>>>(a);
     }
     if (grad) {
         const int64_t dh_tiles = ncols * (a.Bp / kGradTile), dh_grid = ((dh_tiles > kSmDhSlots ? dh_tiles : kSmDhSlots) + 7) / 8 * 8;
@@ -960,7 +1070,7 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
             const int64_t lt = (live + kTM - 1) / kTM;
             if (narrow) {
                 launch_narrow<DT, true>(a, l0, lt * kTM, span_of(lt * kTM), s);
-            } else if (!one) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
+            } else if (!one && !a.keep) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
             const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols;
             k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);

@@ -267,6 +267,7 @@ struct SoftmaxArgs {
     // workspace
     int64_t tn;             // rows per tile of the logits passes: sm_row_tile
     bool narrow;            // one row tile of 128 and a long label space: the streaming kernels
+    bool keep;              // the first pass leaves its exponentials in dz: sm_keep
     int64_t Bp, Hp;         // B and H rounded up to tn and 64
     int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
     int32_t* nv;
@@ -275,6 +276,10 @@ struct SoftmaxArgs {
     int slices;             // sm_slices(B)
     float* hit;             // slices x Bp: shares of the mean logit of the row's labels
     float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
+    float* ref;             // Bp: dz holds softmax x 2^(clse - ref)
+    int32_t* redo;          // Bp / tn + 1: row tiles (and, first, whether there are any) to form again
+    int32_t* own;           // blocks of 256 labels: entries of y_col that fall into the block
+    uint16_t* hs;           // Bp x Hp: h x 2^(ref - clse); hc itself unless keep
     float* part;            // label tiles x Bp x (max, sum), units of log 2
     float* rest;            // rest_cap: by place in y_col, what rounding left of the label's entry of D
     int64_t rest_cap;
@@ -294,6 +299,13 @@ constexpr int64_t sm_row_tile(int64_t B, int64_t H, int64_t L)
     return B > 128 && H > 256 && ((B + 255) / 256) * ((L + 255) / 256) >= 256 ? 256 : 128;
 }
 constexpr bool sm_narrow(int64_t B, int64_t H, int64_t L) { return B <= 128 && H <= 1024 && L >= 4096; }
+// Whether the exponentials of all labels are kept (given the workspace for
+// them, bf16 only).
+constexpr int64_t kSmKeepMost = 2LL << 30;      // entries
+constexpr bool sm_keep(int64_t Bp, int64_t tn, int64_t Lr) 
+{
+    return tn == 256 && Lr > kSmLabelTile && Bp * Lr <= kSmKeepMost;
+}
 constexpr int64_t kSmNarrowSlots = 256;   // workgroups of those kernels: one per CU
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
 constexpr int64_t kSmRest = 64;        // places of y_col per row that are corrected for rounding, on average

@@ -104,6 +104,43 @@ def test_softmax(case, t):
     assert all(torch.equal(again[k], ref[k]) for k in ref), "not repeatable"
 
 
+# large enough that the exponentials of all labels are kept: labels spread over the whole space, over few blocks of 256 (lists
+# of a block that hold each label's remainder too, hold it alone, overflow), many a row, rows beyond the kept range
+KEPT = {"spread": (260, 264, 33_001, 4, None, 2.5), "many": (515, 296, 22_100, 90, None, 2.5),
+        "heavy": (512, 264, 33_001, 300, None, 2.5),
+        "crowded": (1030, 264, 13_100, 5, 2500, 2.5), "overflowing": (1030, 264, 13_100, 5, 700, 2.5),
+        "large": (300, 264, 33_001, 3, None, 40.0), "low": (300, 264, 33_001, 3, None, 2.5)}
+
+
+@pytest.mark.parametrize("name", KEPT)
+def test_kept_exponentials(name):
+    """h is rounded once more on the way to dW here (times the row's factor): half a step of every product's share."""
+    B, H, L, m, over, gain = KEPT[name]
+    h, W, h64, W64, rp, col = make(B, H, over or L, m, 0.15, "bf16", B + L, gain)
+    if over:
+        W, W64 = rounded(np.random.default_rng(9).normal(size=(L, H)) * (gain / np.sqrt(H)), "bf16")
+    if name == "low":           # a third of the rows: every logit near -50 or near +50
+        W[:, 0], W64[:, 0] = 1.0, 1.0
+        for b in range(0, B, 3):
+            if rp[b + 1] > rp[b]:
+                h[b, 0] = h64[b, 0] = -50.0 if b % 2 else 50.0
+    scale = 1.0 / B
+    say(f"  kept exponentials {name}")
+    want = F.oracle_softmax(np.nan_to_num(h64, posinf=0), W64, rp, col, scale)
+    b = bounds(h64, W64, want, rp, scale, "bf16")
+    live = np.diff(rp) > 0
+    more = scale * u("bf16") * (np.abs(want["D"]).T @ np.where(live[:, None], np.abs(np.nan_to_num(h64, posinf=0)), 0))
+    args = put(h), put(W), put(torch.from_numpy(rp)), put(torch.from_numpy(col))
+    ws = torch.full((hs.softmax_workspace_size(B, H, L),), 0xFF, dtype=torch.uint8, device=dev())
+    out = hs.softmax_step(*args, scale, workspace=ws)
+    check(out, want, b | {"dW": b["dW"] + 1.02 * more})
+    again = hs.softmax_step(*args, scale)
+    assert all(torch.equal(again[k], out[k]) for k in out), "not repeatable"
+    some = hs.softmax_workspace_size(B, H, L, minimum=True) + (4 << 20)         # a few pieces: nothing is kept
+    pieces = hs.softmax_step(*args, scale, workspace=ws[:some])
+    check(pieces, want, b)
+
+
 def test_all_rows_padding():
     B, H, L = 70, 96, 300
     h = torch.full((B, H), float("nan"), dtype=torch.bfloat16, device=dev())
