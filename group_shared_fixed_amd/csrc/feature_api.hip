@@ -49,7 +49,7 @@ int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_d
 struct SoftmaxLayout {
     int64_t tn, Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
     bool keep;                       // the pieces may be one, of all labels, past the cap
-    size_t nv, rows, rank, hit, clse, part, rest, ref, redo, own, hc, hs, dhp, dz;
+    size_t nv, rows, rank, hit, clse, part, rest, slot, own, ref, redo, hc, hs, dhp, dz;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
     {
         tn = sm_row_tile(B, H, L);
@@ -57,7 +57,7 @@ struct SoftmaxLayout {
         Hp = round_up(H, 64);
         Lr = round_up(L, kSmLabelTile);
         const int64_t most = (256LL << 20) / (2 * Bp) / kSmLabelTile * kSmLabelTile;
-        keep = grad && sm_keep(Bp, tn, Lr);
+        keep = grad && sm_keep(B, Bp, Lr);
         want = keep ? Lr : balanced(most < kSmLabelTile ? kSmLabelTile : most);
         const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / 128);
         size_t at = 0;
@@ -75,9 +75,10 @@ struct SoftmaxLayout {
         const int64_t parts = Lr / kSmLabelTile;
         part = take((size_t)(parts > kSmNarrowSlots ? parts : kSmNarrowSlots) * (size_t)Bp * 8);
         rest = grad ? take((size_t)(Bp * kSmRest) * 4) : at;
+        slot = grad ? take((size_t)(Bp * kSmRest) * 4) : at;
+        own = grad ? take((size_t)(Lr / kSmLabelTile) * 4) : at;
         ref = keep ? take((size_t)Bp * 4) : at;
         redo = keep ? take((size_t)(Bp / tn + 1) * 4) : at;
-        own = keep ? take((size_t)(Lr / kSmLabelTile) * 4) : at;
         hc = take((size_t)Bp * (size_t)Hp * 2);
         hs = keep ? take((size_t)Bp * (size_t)Hp * 2) : hc;
         dhp = grad ? take((size_t)(tiles > kSmDhSlots ? tiles : kSmDhSlots) * (size_t)(128 * kSmLabelTile) * 4) : at;
@@ -138,6 +139,7 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.ref = (float*)(w + l.ref);
     a.redo = (int32_t*)(w + l.redo);
     a.own = (int32_t*)(w + l.own);
+    a.slot = (int32_t*)(w + l.slot);
     a.hc = (uint16_t*)(w + l.hc);
     a.hs = a.keep ? (uint16_t*)(w + l.hs) : a.hc;
     a.dhp = (float*)(w + l.dhp);

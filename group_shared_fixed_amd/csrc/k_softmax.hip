@@ -49,17 +49,12 @@ __device__ __forceinline__ int64_t dz_at(const SoftmaxArgs& a, int64_t rank, int
 }
 
 // rows / rank / nv: the ranks of the rows that have labels, in row order.
-// Also clears what the passes of `keep` count in.
 __global__ __launch_bounds__(1024) void k_sm_rows(SoftmaxArgs a)
 {
     __shared__ int32_t cnt[1024];
     const int t = threadIdx.x;
     const int64_t B = a.B;
     const int32_t* __restrict__ const rowptr = a.y_rowptr;
-    if (a.keep) {
-        for (int64_t i = t; i < a.Lc / kTM; i += 1024) a.own[i] = a.count[i] = 0;
-        for (int64_t i = t; i <= a.Bp / a.tn; i += 1024) a.redo[i] = 0;
-    }
     const int64_t per = (B + 1023) / 1024, b0 = t * per, b1 = b0 + per < B ? b0 + per : B;
     int n = 0;
     for (int64_t b = b0; b < b1; ++b) n += rowptr[b + 1] > rowptr[b];
@@ -144,14 +139,55 @@ __device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* 
     return wave_sum(s);
 }
 
+// own / slot of the g-th share of the blocks of 256 labels, in passes over all of
+// y_col: counted in LDS, since hot labels' global counters are a queue (640 us
+// at 4096 rows of 36 of 5000 labels).  With more labels than all lists can
+// take, no block gets one.
+__device__ __forceinline__ void count_labels(const SoftmaxArgs& a, int64_t g)
+{
+    __shared__ int32_t cnt[kSmBucket];
+    const int t = threadIdx.x;
+    const int64_t blocks = (a.L + kTM - 1) / kTM, per = (blocks + kSmBuckets - 1) / kSmBuckets, first = g * per;
+    const int64_t left = blocks - first;
+    const int n = (int)(left < per ? left : per);
+    if (n <= 0) return;
+    const int64_t p0 = a.y_rowptr[0], p1 = a.y_rowptr[a.B];
+    if (per > kSmBucket || p1 - p0 > blocks * kSmList) {
+        for (int i = t; i < n; i += 256) a.own[first + i] = kSmList + 1;
+        return;
+    }
+    for (int i = t; i < n; i += 256) cnt[i] = 0;
+    __syncthreads();
+    constexpr int U = 16;
+    const int64_t end = p1 < a.rest_cap ? p1 : a.rest_cap;
+    for (int64_t p = p0 + t; p < end; p += 256 * U) {
+        int32_t l[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) l[u] = p + 256 * u < end ? a.y_col[p + 256 * u] : -1;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t b = l[u] / kTM - first;
+            if (l[u] >= 0 && l[u] < a.L && b >= 0 && b < n) a.slot[p + 256 * u] = atomicAdd(cnt + b, 1);
+        }
+    }
+    __syncthreads();
+    for (int i = t; i < n; i += 256) a.own[first + i] = cnt[i];
+}
+
 // Workgroup (i, y): the mean logit of the labels 4 y .., 16 at a time, of rank
 // i's row (its share of it: hit[y][i]); y = 0 also copies the row into hc
-// (zeros past nv and past H).
+// (zeros past nv and past H).  For a step kSmBuckets more in x count the labels.
 template <int DT, bool FEW>
 __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
 {
     __shared__ float sh[4];
     const int64_t i = blockIdx.x;
+    if (i >= a.Bp) {
+        if (blockIdx.y == 0) count_labels(a, i - a.Bp);
+        if (a.keep && blockIdx.y == 1 && i == a.Bp)
+            for (int64_t k = threadIdx.x; k <= a.Bp / a.tn; k += 256) a.redo[k] = 0;
+        return;
+    }
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int64_t b;
     bool live;
@@ -173,12 +209,7 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
     float s = 0.f;
     for (int p = p0 + 4 * blockIdx.y + w; p < p1; p += 4 * (int)gridDim.y) {
         const int64_t l = a.y_col[p];
-        if (l < 0 || l >= a.L) continue;
-        s += wave_dot<DT>(a, src, l, lane);
-        // how many entries the block's list will have (a count past the limit may stay where it is)
-        if (a.keep && lane == 0 && a.B <= a.L &&
-            __hip_atomic_load(a.own + l / kTM, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) <= kSmList)
-            atomicAdd(a.own + l / kTM, 1);
+        if (l >= 0 && l < a.L) s += wave_dot<DT>(a, src, l, lane);
     }
     if (lane == 0) sh[w] = s;
     __syncthreads();
@@ -523,10 +554,13 @@ __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
     }
 }
 
+// Entries of the list of a block with n labels' places, each.
+__device__ __forceinline__ int kept_each(int n) { return n > kSmList ? 0 : 2 * n <= kSmList ? 2 : 1; }
+
 // A label's own entry d = p - 1 / m where the exponentials are kept.  It leaves
-// dz for the block's list, as one or two of its entries (its rounding and, over
-// a quarter of a step, what that leaves), so that it meets h itself in dW and
-// is exact in dh; in blocks that have too many, its place in dz takes it.
+// dz for the block's list (rounded, and in a second entry what that leaves,
+// where all labels' two fit), so that it meets h itself in dW and is exact in
+// dh; in blocks that have too many, its place in dz takes it.
 template <int DT>
 __device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t i, int64_t l, float d, float up2)
 {
@@ -534,7 +568,7 @@ __device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t 
     const int n = a.own[block];
     uint16_t* const at = a.dz + dz_at(a, i, l);
     float hi, none;
-    if (a.B > a.L || n > kSmList || p >= a.rest_cap) {
+    if (n > kSmList || p >= a.rest_cap) {
         const uint32_t v = pack2<DT>(d * __builtin_amdgcn_exp2f(up2), 0.f);
         *at = (uint16_t)v;
         unpack2<DT>(v, hi, none);
@@ -544,12 +578,11 @@ __device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t 
     *at = 0;
     a.rest[p] = d;
     unpack2<DT>(pack2<DT>(d, 0.f), hi, none);
-    const bool two = 2 * n <= kSmList && fabsf(d - hi) > fabsf(d) * 0x1p-10f;
-    const int32_t slot = atomicAdd(a.count + block, two ? 2 : 1);       // the reader sorts
-    u32x4_t* const to = a.list + block * kSmList + slot;
+    const int each = kept_each(n);
+    u32x4_t* const to = a.list + block * kSmList + a.slot[p] * each;
     const uint32_t where = (uint32_t)i | (uint32_t)(l % kTM) << 20;
     to[0] = u32x4_t{2 * (uint32_t)p, where, __float_as_uint(hi), 0u};
-    if (two) to[1] = u32x4_t{2 * (uint32_t)p + 1, where, __float_as_uint(d - hi), 0u};
+    if (each == 2) to[1] = u32x4_t{2 * (uint32_t)p + 1, where, __float_as_uint(d - hi), 0u};
 }
 
 // The labels' own entries of D in the piece [l0, l0 + Lc): workgroups as in
@@ -590,16 +623,12 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
                 float up, none;
                 unpack2<DT>(hi, up, none);
                 if (p < a.rest_cap) a.rest[p] = d - up;
-                // the list is for the larger half: over a quarter of a step of the type at d.
-                // (With more rows than labels the blocks' lists would overflow, and the waves queue for
-                // their counters: 417 rows of 36 of 217 labels, 48 us instead of 6.)
-                if (a.B > a.L) continue;
-                if (fabsf(d - up) <= fabsf(d) * (DT == HASTE_F16 ? 0x1p-12f : 0x1p-9f)) continue;
-                // (a list that is past its length stays so: no more atomics on its counter)
-                int32_t* const count = a.count + (l - l0) / kTM;
-                if (__hip_atomic_load(count, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) > kSmList) continue;
+                // the list is for the larger half: over a quarter of a step of the type at d, in blocks
+                // whose list holds all (in the others the waves would queue for its counter)
+                if (fabsf(d - up) <= fabsf(d) * (DT == HASTE_F16 ? 0x1p-12f : 0x1p-9f) || a.own[l / kTM] > kSmList)
+                    continue;
                 const int64_t block = (l - l0) / kTM;
-                const int32_t slot = atomicAdd(count, 1);               // the reader sorts
+                const int32_t slot = atomicAdd(a.count + block, 1);     // the reader sorts
                 if (slot < kSmList)
                     a.list[block * kSmList + slot] =
                         u32x4_t{(uint32_t)p, (uint32_t)i | (uint32_t)((l - l0) % kTM) << 20, __float_as_uint(d - up), 0u};
@@ -698,7 +727,13 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
     const Operand A{a.hs, a.Hp, a.Hp, a.Bp};
     const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
     // the block's list, whole: what lies past its length is not used
-    const int rest = nv > 0 ? a.count[n0 / kTM] : 0;
+    int rest = 0;
+    if (nv > 0 && a.keep) {
+        const int own = a.own[n0 / kTM];
+        rest = own * kept_each(own);
+    } else if (nv > 0) {
+        rest = a.count[n0 / kTM];
+    }
     u32x4_t mine[kPerThread<TN>];
 #pragma unroll
     for (int i = 0; i < kPerThread<TN>; ++i) mine[i] = a.list[n0 / kTM * kSmList + threadIdx.x + kThreads<TN> * i];
@@ -1037,11 +1072,12 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
     constexpr int NT = kThreads<TN>;
     const int64_t nrt = a.Bp / TN, tiles = (a.L + kTM - 1) / kTM, ncols = (a.Hp + kTM - 1) / kTM;
     const dim3 by_rank((unsigned)a.Bp, (unsigned)a.slices);
-    if (a.B <= kFewRows && !a.keep) {
-        k_sm_gather<DT, true><<<by_rank, 256, 0, s>>>(a);
+    const dim3 gather((unsigned)(a.Bp + (grad ? kSmBuckets : 0)), (unsigned)a.slices);
+    if (a.B <= kFewRows) {
+        k_sm_gather<DT, true><<<gather, 256, 0, s>>>(a);
     } else {
         k_sm_rows<<<1, 1024, 0, s>>>(a);
-        k_sm_gather<DT, false><<<by_rank, 256, 0, s>>>(a);
+        k_sm_gather<DT, false><<<gather, 256, 0, s>>>(a);
     }
     const bool one = tiles == 1;
     const bool narrow = TN == 128 && a.narrow;
@@ -1054,13 +1090,13 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
         k_sm_logits<DT, TN, kOneTile><<<(unsigned)nrt, NT, 0, s>>>(a, 0, grad);
     } else {
         bool kept = false;
-        if constexpr (DT == HASTE_BF16 && TN == 256) {
+        if constexpr (DT == HASTE_BF16) {
             if (a.keep) k_sm_logits<DT, TN, kKeep><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
             kept = a.keep;
         }
         if (!kept) k_sm_logits<DT, TN, kStatistics><<<(unsigned)(tiles * nrt), NT, 0, s>>>(a, 0, false);
         k_sm_lse<<<(unsigned)((a.Bp + 7) / 8), 256, 0, s>>>(a, tiles);
-        if constexpr (DT == HASTE_BF16 && TN == 256)
+        if constexpr (DT == HASTE_BF16)
             if (kept) k_sm_redo<DT, TN><<<256, NT, 0, s>>>(a);
     }
     if (grad) {

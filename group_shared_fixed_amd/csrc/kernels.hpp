@@ -278,7 +278,8 @@ struct SoftmaxArgs {
     float* clse;            // Bp: log2-sum-exp by rank (units of log 2)
     float* ref;             // Bp: dz holds softmax x 2^(clse - ref)
     int32_t* redo;          // Bp / tn + 1: row tiles (and, first, whether there are any) to form again
-    int32_t* own;           // blocks of 256 labels: entries of y_col that fall into the block
+    int32_t* own;           // blocks of 256 labels of the whole space: places of y_col, below rest_cap, of their labels
+    int32_t* slot;          // rest_cap: each such place's number within its block
     uint16_t* hs;           // Bp x Hp: h x 2^(ref - clse); hc itself unless keep
     float* part;            // label tiles x Bp x (max, sum), units of log 2
     float* rest;            // rest_cap: by place in y_col, what rounding left of the label's entry of D
@@ -301,10 +302,12 @@ constexpr int64_t sm_row_tile(int64_t B, int64_t H, int64_t L)
 constexpr bool sm_narrow(int64_t B, int64_t H, int64_t L) { return B <= 128 && H <= 1024 && L >= 4096; }
 // Whether the exponentials of all labels are kept (given the workspace for
 // them, bf16 only).
+// Workgroups that count the labels by block, and blocks each can take.
+constexpr int64_t kSmBuckets = 64, kSmBucket = 2048;
 constexpr int64_t kSmKeepMost = 2LL << 30;      // entries
-constexpr bool sm_keep(int64_t Bp, int64_t tn, int64_t Lr) 
+constexpr bool sm_keep(int64_t B, int64_t Bp, int64_t Lr)
 {
-    return tn == 256 && Lr > kSmLabelTile && Bp * Lr <= kSmKeepMost;
+    return B > 128 && Lr > kSmLabelTile && (B + 255) / 256 * (Lr / kSmLabelTile) >= 256 && Bp * Lr <= kSmKeepMost;
 }
 constexpr int64_t kSmNarrowSlots = 256;   // workgroups of those kernels: one per CU
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
