@@ -49,7 +49,8 @@ int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_d
 struct SoftmaxLayout {
     int64_t tn, Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
     bool keep;                       // the pieces may be one, of all labels, past the cap
-    size_t nv, rows, rank, hit, clse, part, rest, slot, own, ref, redo, hc, hs, dhp, dz;
+    size_t nv, rows, rank, hit, clse, part, rest, slot, own, ref, redo, hc, hs, dhp, dwp, dz;
+    int64_t dws;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
     {
         tn = sm_row_tile(B, H, L);
@@ -82,6 +83,8 @@ struct SoftmaxLayout {
         hc = take((size_t)Bp * (size_t)Hp * 2);
         hs = keep ? take((size_t)Bp * (size_t)Hp * 2) : hc;
         dhp = grad ? take((size_t)(tiles > kSmDhSlots ? tiles : kSmDhSlots) * (size_t)(128 * kSmLabelTile) * 4) : at;
+        dws = grad ? sm_dw_splits(Bp, Hp, Lr) : 1;
+        dwp = dws > 1 ? take((size_t)(dws * Lr * Hp) * 4) : at;
         dz = at;
     }
     int64_t balanced(int64_t most) const
@@ -143,6 +146,8 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.hc = (uint16_t*)(w + l.hc);
     a.hs = a.keep ? (uint16_t*)(w + l.hs) : a.hc;
     a.dhp = (float*)(w + l.dhp);
+    a.dw_splits = a.Lc == l.Lr ? (int)l.dws : 1;
+    a.dwp = (float*)(w + l.dwp);
     a.rest = (float*)(w + l.rest);
     a.rest_cap = l.Bp * kSmRest;
     a.dz = (uint16_t*)(w + l.dz);

@@ -493,7 +493,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 // Forms the kept exponentials again, as probabilities, of rows whose logits lie
 // too far from 0 (and of the other rows of their tiles, as they were).
 template <int DT, int TN>
-__global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_redo(SoftmaxArgs a)
+__global__ __launch_bounds__(kThreads<TN>, 1) void k_sm_redo(SoftmaxArgs a)
 {
     HASTE_SM_RING(TN)
     __shared__ float red[2][TN][2];
@@ -717,18 +717,44 @@ __device__ __forceinline__ void add_rest(const SoftmaxArgs& a, int64_t n0, int64
     }
 }
 
-// dW of one tile of 256 columns x TN labels of the piece.
+// A wave's 128 x 64 tile as 64 fp32 rows of a partial, from column j0 on: stored
+// or added.
+__device__ __forceinline__ void store_partial(float* out, int64_t Hp, int64_t j0, const f32x16_t (&acc)[4][2], bool first)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t j = j0 + 32 * mt + 8 * g + 4 * (lane >> 5);
+                if (j >= Hp) continue;
+                f32x4_t* o = reinterpret_cast<f32x4_t*>(out + (32 * nt + (lane & 31)) * Hp + j);
+                f32x4_t v = {acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2], acc[mt][nt][4 * g + 3]};
+                if (!first) v += *o;
+                *o = v;
+            }
+}
+
+// dW of one tile of 256 columns x TN labels of the piece, over one range of rows.
 template <int DT, int TN>
 __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_t ncols, int64_t t,
                                         uint16_t* const (&ring)[3])
 {
+    const int S = a.dw_splits, s = (int)(t % S);
+    t /= S;
     const int64_t m0 = t % ncols * kTM, n0 = t / ncols * TN;
-    const int nv = *a.nv;
-    const Operand A{a.hs, a.Hp, a.Hp, a.Bp};
-    const Operand B{a.dz + dz_at(a, 0, n0), kTM, TN, a.Bp};
+    const int nv = *a.nv, stages = (nv + kStage<TN> - 1) / kStage<TN>, len = (stages + S - 1) / S;
+    const int64_t r0 = (int64_t)s * len * kStage<TN>;
+    const int nst = len < stages - s * len ? len : stages - s * len;
+    const Operand A{a.hs + r0 * a.Hp, a.Hp, a.Hp, a.Bp - r0};
+    const Operand B{a.dz + dz_at(a, r0, n0), kTM, TN, a.Bp - r0};
     // the block's list, whole: what lies past its length is not used
     int rest = 0;
-    if (nv > 0 && a.keep) {
+    if (s > 0) {
+        rest = 0;
+    } else if (nv > 0 && a.keep) {
         const int own = a.own[n0 / kTM];
         rest = own * kept_each(own);
     } else if (nv > 0) {
@@ -738,9 +764,13 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
 #pragma unroll
     for (int i = 0; i < kPerThread<TN>; ++i) mine[i] = a.list[n0 / kTM * kSmList + threadIdx.x + kThreads<TN> * i];
     f32x16_t acc[4][2];
-    tile_product<DT, TN, true, true>(A, m0, B, 0, (nv + kStage<TN> - 1) / kStage<TN>, ring, acc);
+    tile_product<DT, TN, true, true>(A, m0, B, 0, nst, ring, acc);
     add_rest<DT, TN>(a, n0, m0, rest, mine, ring, acc);
     const int wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
+    if (S > 1) {
+        store_partial(a.dwp + ((int64_t)s * a.Lc + n0 + 64 * wn) * a.Hp, a.Hp, m0 + 128 * wm, acc, true);
+        return;
+    }
     const float f = a.scale / kDScale<DT>;
     uint16_t* const dW = reinterpret_cast<uint16_t*>(a.dW);
     const int64_t l = l0 + n0 + 64 * wn, j = m0 + 128 * wm;
@@ -785,22 +815,8 @@ __device__ __forceinline__ void dh_tile(const SoftmaxArgs& a, int64_t l0, int64_
     const Operand B{a.dz + dz_at(a, 0, k0), kTM, a.Bp, a.Lc - k0, a.Bp * kTM};
     f32x16_t acc[4][2];
     tile_product<DT, TN, true, false, true>(A, m0, B, n0, (int)((k1 - k0) / kStage<TN>), ring, acc);
-    const int lane = threadIdx.x & 63, wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        const int64_t n = n0 + 64 * wn + 32 * nt + (lane & 31);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t j = m0 + 128 * wm + 32 * mt + 8 * g + 4 * (lane >> 5);
-                if (j >= a.Hp) continue;
-                f32x4_t* o = reinterpret_cast<f32x4_t*>(a.dhp + (s * nvt * TN + n) * a.Hp + j);
-                f32x4_t v = {acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2], acc[mt][nt][4 * g + 3]};
-                if (!first) v += *o;
-                *o = v;
-            }
-    }
+    const int wm = (threadIdx.x >> 6) & 1, wn = threadIdx.x >> 7;
+    store_partial(a.dhp + (s * nvt * TN + n0 + 64 * wn) * a.Hp, a.Hp, m0 + 128 * wm, acc, first);
 }
 
 // Both gradients of a piece in one launch: dW has its stores where dh has its
@@ -994,10 +1010,11 @@ void launch_narrow(const SoftmaxArgs& a, int64_t l0, int64_t n, int64_t span, hi
     else k_sm_narrow<DT, 32, GRAD><<<g, 512, 0, s>>>(a, l0, n, span);
 }
 
-// dh by row from the partials (0 for rows without labels); workgroup 0 also
-// adds up the loss, in 64 bits and a fixed order.
+// dh by row from the partials (0 for rows without labels), dW by label where it
+// was split over the rows; workgroup 0 adds up the loss, in 64 bits and a fixed
+// order.
 template <int DT>
-__global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int64_t ncols)
+__global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int64_t ncols, uint32_t first_dw)
 {
     if (blockIdx.x == 0) {
         __shared__ double sh[256];
@@ -1013,6 +1030,23 @@ __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int
         return;
     }
     if (!grad) return;
+    if (blockIdx.x >= first_dw) {       // dW from its partials, eight columns per thread
+        const int64_t per = a.H / 8, u = (int64_t)(blockIdx.x - first_dw) * 256 + threadIdx.x;
+        if (u >= a.L * per) return;
+        const int64_t l = u / per, j = 8 * (u % per);
+        float v[8] = {};
+#pragma unroll 4
+        for (int s = 0; s < a.dw_splits; ++s) {
+            float w[8];
+            widen8<HASTE_F32>(load8<HASTE_F32>(a.dwp, ((int64_t)s * a.Lc + l) * a.Hp + j, 8), w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += w[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= a.scale / kDScale<DT>;
+        store8<DT>(a.dW, l * a.H + j, 8, v);
+        return;
+    }
     // 32 runs of eight columns per workgroup, eight threads each over the partials
     __shared__ float part[8][32][9];
     const int64_t per = a.H / 8, n = a.B * per;
@@ -1108,12 +1142,13 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
                 launch_narrow<DT, true>(a, l0, lt * kTM, span_of(lt * kTM), s);
             } else if (!one && !a.keep) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
-            const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols;
+            const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols * a.dw_splits;
             k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);
         }
     }
     const int64_t blocks = grad ? (a.B * (a.H / 8) + 31) / 32 : 0;
-    k_sm_finish<DT><<<(unsigned)(1 + blocks), 256, 0, s>>>(a, grad, ncols);
+    const int64_t dw = grad && a.dw_splits > 1 ? (a.L * (a.H / 8) + 255) / 256 : 0;
+    k_sm_finish<DT><<<(unsigned)(1 + blocks + dw), 256, 0, s>>>(a, grad, ncols, (uint32_t)(1 + blocks));
 }
 
 template <int DT>

@@ -288,6 +288,8 @@ struct SoftmaxArgs {
     u32x4_t* list;          // kSmList per block: (place in y_col, rank | label << 20, rest, 0)
     uint16_t* hc;           // Bp x Hp
     uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
+    int dw_splits;          // row ranges that dW is formed over
+    float* dwp;             // their partials (ranges x labels in whole tiles of 128 x Hp), if several
     float* dhp;             // partials of dh, at most max(kSmDhSlots, tiles) tiles of 256 x 128
 };
 constexpr int64_t kSmLabelTile = 256;
@@ -307,12 +309,20 @@ constexpr int64_t kSmBuckets = 64, kSmBucket = 2048;
 constexpr int64_t kSmKeepMost = 2LL << 30;      // entries
 constexpr bool sm_keep(int64_t B, int64_t Bp, int64_t Lr)
 {
-    return B > 128 && Lr > kSmLabelTile && (B + 255) / 256 * (Lr / kSmLabelTile) >= 256 && Bp * Lr <= kSmKeepMost;
+    return B > 128 && Lr > kSmLabelTile && (B + 255) / 256 * (Lr / kSmLabelTile) >= 64 && Bp * Lr <= kSmKeepMost;
 }
 constexpr int64_t kSmNarrowSlots = 256;   // workgroups of those kernels: one per CU
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
 constexpr int64_t kSmRest = 64;        // places of y_col per row that are corrected for rounding, on average
 constexpr int kSmList = 512;           // and entries per block of 256 labels
+// Row ranges of dW: where its tiles would leave the chip idle over a long
+// contraction, as many as fill it, of 512 rows at least.
+constexpr int64_t sm_dw_splits(int64_t Bp, int64_t Hp, int64_t Lr)
+{
+    const int64_t tiles = Lr / 128 * ((Hp + 255) / 256), fill = kSmDhSlots / tiles, most = Bp / 512;
+    const int64_t s = fill < most ? fill : most;
+    return s < 1 ? 1 : s;
+}
 // Workgroups that share a row's labels: few rows may have many each, and fill
 // the chip only that way.
 constexpr int sm_slices(int64_t B) { return B <= 256 ? 16 : 4; }

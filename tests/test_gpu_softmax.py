@@ -73,7 +73,9 @@ CASES = [  # B, H, L, m, empty
     (16, 64, 4096, 5, 0), (33, 72, 515, 4, 0.5), (64, 256, 2000, 8, 0.2), (128, 768, 2048, 32, 0),
     (130, 264, 1001, 4, 0.4), (257, 1000, 700, 1, 0.6), (300, 96, 513, 40, 0.95), (515, 520, 1300, 2, 0.3),
     # one row tile over a long label space: ranges of the streaming kernels that end inside tiles, pieces and the last label
-    (1, 1032, 4097, 1, 0), (20, 264, 5003, 4, 0.2), (128, 768, 4500, 30, 0), (97, 1000, 20011, 2, 0.4), (128, 64, 70001, 1, 0.1)]
+    (1, 1032, 4097, 1, 0), (20, 264, 5003, 4, 0.2), (128, 768, 4500, 30, 0), (97, 1000, 20011, 2, 0.4), (128, 64, 70001, 1, 0.1),
+    # many rows, few labels: dW over ranges of rows, of which the last may be empty
+    (1100, 64, 70, 5, 0.2), (2200, 520, 600, 3, 0.5), (4100, 72, 300, 2, 0.9)]
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp16"])
