@@ -4,12 +4,18 @@
 // lse_b = log sum_l exp z_bl:
 //   row_loss_b = lse_b - (1 / m_b) sum_{l in Y_b} z_bl
 //   D = softmax(z) - [l in Y_b] / m_b,  dW = s D^T h,  dh = s D W.
-// The logits are never kept: a first pass forms them tile by tile and keeps
-// one (maximum, sum) pair per row and 256-label tile; a second pass forms
-// them again, piece of the label space by piece, as D in the workspace (two
-// bytes per entry, Bp x Lc), from which the two gradient products of the
-// piece are taken.  That is eight instead of six B L H operations, against
-// four bytes per logit written and read twice.
+// A first pass forms the logits tile by tile and keeps one (maximum, sum) pair
+// per row and tile.  The gradients then need softmax(z) as an operand:
+//  - kept (a.keep: bf16, more than 128 rows, workspace for all labels): the
+//    first pass stores e = exp z itself, rounded to bf16, whose exponent range
+//    makes a common reference unnecessary.  softmax(z) = e / sum e, so the row's
+//    factor goes to the other operand: dW = (e)^T (h / sum e), and dh's rows
+//    are divided at their end.  Rows whose log-sum-exp lies outside 0 .. 64
+//    octaves are formed again as probabilities.  6 B L H operations and six
+//    bytes per logit.
+//  - else a second pass forms the logits again, piece of the label space by
+//    piece, as D in the workspace (two bytes per entry, Bp x Lc): eight
+//    B L H operations, and no more memory than one piece.
 //
 // Rows without labels are left out: the rows that have some are compacted
 // first (ranks), so padding costs no products and nothing in a padded row
@@ -17,11 +23,18 @@
 //
 // D is rounded to the operands' type for the matrix cores: half a step of
 // relative error per entry, the size of the rounding of dW and dh
-// themselves; in fp16 it is held times 2^12, since probabilities of 1e-5
-// would be subnormal there.  The entries of the labels themselves carry most
-// of the gradient, and with several labels per row they are p - 1 / m, often
-// at the foot of a binade where half a step is largest: what their rounding
-// leaves (k_sm_labels) is added to both gradients.  (With one label, -1 + p rounds well.)
+// themselves (and h / sum e once more, on the way to dW); in fp16 it is held
+// times 2^12, since probabilities of 1e-5 would be subnormal there.  The
+// entries of the labels themselves carry most of the gradient, and with
+// several labels per row they are p - 1 / m, often at the foot of a binade
+// where half a step is largest: what their rounding leaves (k_sm_labels) is
+// added to both gradients.  (With one label, -1 + p rounds well.)  Kept
+// exponentials hold them not at all.
+//
+// Measured, whole step: 4096 x 131072 x 1024 bf16, a quarter of the rows
+// padding, 2.57 ms (963 TFLOP/s of 6 B L H; 3.33 ms with two passes); 128 x
+// 89088 x 768 192 us; 1021 x 32003 x 640 fp16, 40 % padding, 192 us; 37 x 73 x
+// 96 32 us.
 #include "kernels.hpp"
 #include "tile.hpp"
 
@@ -48,7 +61,8 @@ __device__ __forceinline__ int64_t dz_at(const SoftmaxArgs& a, int64_t rank, int
     return (label / kTM * a.Bp + rank) * kTM + label % kTM;
 }
 
-// rows / rank / nv: the ranks of the rows that have labels, in row order.
+// rows / rank / nv: the ranks of the rows that have labels, in row order.  One
+// workgroup, 7 us at 4096 rows.
 __global__ __launch_bounds__(1024) void k_sm_rows(SoftmaxArgs a)
 {
     __shared__ int32_t cnt[1024];
@@ -78,6 +92,7 @@ __global__ __launch_bounds__(1024) void k_sm_rows(SoftmaxArgs a)
 // Batches of up to kFewRows find their ranks in the gather itself (each of
 // its workgroups counts), one launch less.
 constexpr int64_t kFewRows = 1024;
+
 // The row of rank i (or -1) and the number of ranks, by the whole workgroup of
 // 256; PUBLISH also writes rows, rank and nv.
 template <bool PUBLISH>
@@ -139,10 +154,10 @@ __device__ __forceinline__ float wave_dot(const SoftmaxArgs& a, const uint16_t* 
     return wave_sum(s);
 }
 
-// own / slot of the g-th share of the blocks of 256 labels, in passes over all of
-// y_col: counted in LDS, since hot labels' global counters are a queue (640 us
-// at 4096 rows of 36 of 5000 labels).  With more labels than all lists can
-// take, no block gets one.
+// own / slot of the g-th share of the blocks of 256 labels, from all of y_col:
+// counted in LDS, since hot labels' global counters are a queue (540 us for
+// 4096 rows of 36 of 5000 labels; the whole gather is 30 us with this).  With
+// more labels than all lists can take, no block gets one.
 __device__ __forceinline__ void count_labels(const SoftmaxArgs& a, int64_t g)
 {
     __shared__ int32_t cnt[kSmBucket];
@@ -176,7 +191,8 @@ __device__ __forceinline__ void count_labels(const SoftmaxArgs& a, int64_t g)
 
 // Workgroup (i, y): the mean logit of the labels 4 y .., 16 at a time, of rank
 // i's row (its share of it: hit[y][i]); y = 0 also copies the row into hc
-// (zeros past nv and past H).  For a step kSmBuckets more in x count the labels.
+// (zeros past nv and past H).  Bound by the latency of its dependent loads: 6 us
+// for 128 rows of 36 labels, 16 for 4096 of one.  For a step kSmBuckets more in x count the labels.
 template <int DT, bool FEW>
 __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
 {
@@ -220,8 +236,8 @@ __global__ __launch_bounds__(256) void k_sm_gather(SoftmaxArgs a)
 // Tile shapes: 256 x TN, TN = 256 by eight waves or TN = 128 by four; each
 // wave owns 128 x 64 of it (wave w: tile rows 128 (w % 2) .., columns
 // 64 (w / 2) ..).  The wide tile asks L2 for a third fewer operand bytes per
-// product, which is what bounds large products here; the narrow one serves
-// batches of up to 128 rows.
+// product, which is what bounds large logits passes; the narrow one serves
+// small ones (sm_row_tile) and the gradients.
 template <int TN>
 constexpr int kThreads = 2 * TN;
 // The stage ring: R buffers of both operands' tiles.  The wide tile takes two
@@ -472,7 +488,10 @@ __device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, in
     }
 }
 
-// Eight label tiles by the row tiles in turn.
+// Eight label tiles by the row tiles in turn.  Bound by the products and the
+// operands' way from L2 into LDS: 3072 live rows x 131072 x 1024 (statistics)
+// 800 us, 1030 TFLOP/s, of which the products alone are 607; with the
+// exponentials stored (kKeep) 930.  612 live rows x 32003 x 640 fp16 45 us.
 template <int DT, int TN, Pass PASS>
 __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0, bool grad)
 {
@@ -491,7 +510,8 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
 }
 
 // Forms the kept exponentials again, as probabilities, of rows whose logits lie
-// too far from 0 (and of the other rows of their tiles, as they were).
+// too far from 0 (and of the other rows of their tiles, as they were).  Seldom
+// has work: 4 us without.
 template <int DT, int TN>
 __global__ __launch_bounds__(kThreads<TN>, 1) void k_sm_redo(SoftmaxArgs a)
 {
@@ -508,7 +528,8 @@ __global__ __launch_bounds__(kThreads<TN>, 1) void k_sm_redo(SoftmaxArgs a)
 }
 
 // Log-sum-exp of 8 ranks per workgroup from the tiles' pairs, 32 threads per
-// rank; the results by row (0 for rows without labels).
+// rank; the results by row (0 for rows without labels).  5 us at 128 x 348
+// pairs, 9 at 4096 x 512: latency.
 __global__ __launch_bounds__(256) void k_sm_lse(SoftmaxArgs a, int64_t tiles)
 {
     __shared__ float st[32][9], ss[32][9];
@@ -586,7 +607,8 @@ __device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t 
 }
 
 // The labels' own entries of D in the piece [l0, l0 + Lc): workgroups as in
-// k_sm_gather.  The logit is formed again here, in fp32.
+// k_sm_gather.  The logit is formed again here, in fp32.  With kept exponentials
+// also h times the rows' factors.  Latency: 6.6 us for 128 rows of 36 labels.
 template <int DT>
 __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
 {
@@ -637,8 +659,8 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
     }
 }
 
-// acc += sum over a block's list of (what rounding left of an entry of D) x
-// (its row of h): the entries as one more contraction index each, in the
+// acc += sum over a block's list of (what rounding left of an entry of D, or all
+// of it where exponentials are kept) x (its row of h): the entries as one more contraction index each, in the
 // order of the label lists (sorted here, so that the order in which they were
 // appended shows nowhere).  A block with more than kSmList of them goes
 // without.  On return the ring is free.
@@ -783,6 +805,9 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
 
 // The gradients take the narrow tile at every batch: two workgroups per CU
 // fill the chip more evenly with the few tiles and long contractions they have.
+// 3072 live rows x 131072 x 1024 1.58 ms (1044 TFLOP/s); 128 x 89088 x 768
+// 92 us: four stages per tile of dW, whose latency with its list and its
+// 137 MB of stores is half of it.
 constexpr int kGradTile = 128;
 
 // Label ranges that the feature gradient of nv rows is split into: as many
@@ -820,8 +845,9 @@ __device__ __forceinline__ void dh_tile(const SoftmaxArgs& a, int64_t l0, int64_
 }
 
 // Both gradients of a piece in one launch: dW has its stores where dh has its
-// reads of W, and together their last tiles share the chip (4096 x 32768 x 768:
-// 434 us, 488 one after the other on the tiles that are best for each).
+// reads of W, and together their last tiles share the chip (4096 x 131072 x
+// 1024: 3.27 ms a step, 3.29 one after the other on the tiles best for each;
+// 1021 x 32003 x 640 fp16 186 and 201 us).
 // Workgroups [0, dh_grid) take dh.
 template <int DT>
 __global__ __launch_bounds__(256, 2) void k_sm_grads(SoftmaxArgs a, int64_t l0, int64_t ncols, int first,
@@ -838,7 +864,9 @@ __global__ __launch_bounds__(256, 2) void k_sm_grads(SoftmaxArgs a, int64_t l0, 
 // else moves.  One workgroup of eight waves per CU walks a range of labels on
 // a ring of up to eight stages that stays full from the first to the last.
 // (In tiles of 256 labels x 32 columns, as the general pass takes them, the
-// stages of one label row come many microseconds apart.)
+// stages of one label row come many microseconds apart.)  Bound by memory:
+// 128 x 89088 x 768 36 us (3.8 TB/s; the general pass 46), 20 x 57163 x 968
+// fp16 25 us (4.4 TB/s; 40).
 // SW: 32-wide steps of H, a multiple of eight.  LDS image of a stage: piece p
 // of label row r at p ^ r % 16 of the row (a read of 16 rows meets 16 banks).
 // GRAD = false: the range's (maximum, sum) per row into part[workgroup]; true:
@@ -1012,7 +1040,8 @@ void launch_narrow(const SoftmaxArgs& a, int64_t l0, int64_t n, int64_t span, hi
 
 // dh by row from the partials (0 for rows without labels), dW by label where it
 // was split over the rows; workgroup 0 adds up the loss, in 64 bits and a fixed
-// order.
+// order.  Bound by memory and, when small, by latency: 16 us at 128 x 89088 x
+// 768, 38 at 4096 x 131072 x 1024.
 template <int DT>
 __global__ __launch_bounds__(256) void k_sm_finish(SoftmaxArgs a, bool grad, int64_t ncols, uint32_t first_dw)
 {

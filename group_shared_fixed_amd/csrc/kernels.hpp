@@ -282,10 +282,10 @@ struct SoftmaxArgs {
     int32_t* slot;          // rest_cap: each such place's number within its block
     uint16_t* hs;           // Bp x Hp: h x 2^(ref - clse); hc itself unless keep
     float* part;            // label tiles x Bp x (max, sum), units of log 2
-    float* rest;            // rest_cap: by place in y_col, what rounding left of the label's entry of D
+    float* rest;            // rest_cap: by place in y_col, what dz lacks of the label's entry of D
     int64_t rest_cap;
     int32_t* count;         // blocks of 256 labels of a piece: entries appended to the block's list
-    u32x4_t* list;          // kSmList per block: (place in y_col, rank | label << 20, rest, 0)
+    u32x4_t* list;          // kSmList per block: (key by place in y_col, rank | label << 20, value, 0)
     uint16_t* hc;           // Bp x Hp
     uint16_t* dz;           // Bp x Lc, in blocks of 256 labels
     int dw_splits;          // row ranges that dW is formed over
@@ -301,22 +301,31 @@ constexpr int64_t sm_row_tile(int64_t B, int64_t H, int64_t L)
 {
     return B > 128 && H > 256 && ((B + 255) / 256) * ((L + 255) / 256) >= 256 ? 256 : 128;
 }
+// Batches of one row tile of 128 over long label spaces: the streaming logits
+// kernels, whose registers hold up to 1024 columns of the rows (128 x 89088 x
+// 768 36 us a pass, 46 in tiles).
 constexpr bool sm_narrow(int64_t B, int64_t H, int64_t L) { return B <= 128 && H <= 1024 && L >= 4096; }
-// Whether the exponentials of all labels are kept (given the workspace for
-// them, bf16 only).
 // Workgroups that count the labels by block, and blocks each can take.
 constexpr int64_t kSmBuckets = 64, kSmBucket = 2048;
+// Whether the exponentials of all labels are kept (given the workspace for
+// them, bf16 only): where the second pass costs more than the h that is written
+// a second time and the look for rows to form again (us, kept against two
+// passes: 200 x 20000 x 768 92 and 103, 892 x 9527 x 904 160 and 195, 300 x
+// 12000 x 64 53.8 and 53.3).  Batches of up to 128 rows stream W in 35 us
+// where storing and rescaling would take 20, and their dW, sums of few
+// products, would show the rounding of h.
 constexpr int64_t kSmKeepMost = 2LL << 30;      // entries
 constexpr bool sm_keep(int64_t B, int64_t Bp, int64_t Lr)
 {
     return B > 128 && Lr > kSmLabelTile && (B + 255) / 256 * (Lr / kSmLabelTile) >= 64 && Bp * Lr <= kSmKeepMost;
 }
-constexpr int64_t kSmNarrowSlots = 256;   // workgroups of those kernels: one per CU
+constexpr int64_t kSmNarrowSlots = 256;   // workgroups of the streaming kernels: one per CU
 constexpr int64_t kSmDhSlots = 512;    // workgroups of the feature gradient that run at once
 constexpr int64_t kSmRest = 64;        // places of y_col per row that are corrected for rounding, on average
 constexpr int kSmList = 512;           // and entries per block of 256 labels
 // Row ranges of dW: where its tiles would leave the chip idle over a long
-// contraction, as many as fill it, of 512 rows at least.
+// contraction, as many as fill it, of 512 rows at least (us, against one range:
+// 3411 x 83 x 320 72 and 108, 4096 x 1500 x 1024 170 and 181).
 constexpr int64_t sm_dw_splits(int64_t Bp, int64_t Hp, int64_t Lr)
 {
     const int64_t tiles = Lr / 128 * ((Hp + 255) / 256), fill = kSmDhSlots / tiles, most = Bp / 512;
