@@ -77,6 +77,7 @@ SIGNATURES = {
     "haste_score_a8w8": (_M, [_P, _P, _P, _P, _P, _I, _I, _I, _P]),
     "haste_softmax_workspace_size": (_S, [_I, _I, _I, _M]),
     "haste_softmax_workspace_min": (_S, [_I, _I, _I, _M]),
+    "haste_softmax_workspace_whole": (_S, [_I, _I, _I]),
     "haste_softmax_loss": (_M, [_P, _P, _P, _P, _F, _P, _P, _P, _I, _I, _I, _I, _I, _M, _P, _S, _P]),
     "haste_softmax_step": (_M, [_P, _P, _P, _P, _F, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _M, _P, _S, _P]),
     "haste_test_set_turn_spins": (None, [_M]),
@@ -852,9 +853,12 @@ def score_a8w8(hq, h_scale, Wq, w_scale, Z=None, stream=None):
     return Z
 
 
-def softmax_workspace_size(B, H, L, grad=True, minimum=False) -> int:
+def softmax_workspace_size(B, H, L, grad=True, minimum=False, whole=False) -> int:
     """Workspace bytes of softmax_step (grad) or softmax_loss; minimum: the least that is accepted, which
-    takes the label space 256 labels at a time."""
+    takes the label space 256 labels at a time; whole: what lets a bf16 step of more than 128 rows form
+    its logits once (two bytes per logit, up to 4 GiB)."""
+    if whole and grad:
+        return int(lib().haste_softmax_workspace_whole(B, H, L))
     fn = lib().haste_softmax_workspace_min if minimum else lib().haste_softmax_workspace_size
     return int(fn(B, H, L, int(grad)))
 

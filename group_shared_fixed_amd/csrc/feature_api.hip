@@ -48,7 +48,7 @@ int make_drop(double p, uint64_t seed, uint64_t offset, const uint64_t* offset_d
 // from the bytes that are left.
 struct SoftmaxLayout {
     int64_t tn, Bp, Hp, Lr, want;    // want: labels per piece that fill the cap, balanced over the pieces
-    bool keep;                       // the pieces may be one, of all labels, past the cap
+    bool keep;                       // a bf16 step keeps the first piece's exponentials
     size_t nv, rows, rank, hit, clse, part, rest, slot, own, ref, redo, hc, hs, dhp, dwp, dz;
     int64_t dws;
     SoftmaxLayout(int64_t B, int64_t H, int64_t L, bool grad)
@@ -59,7 +59,7 @@ struct SoftmaxLayout {
         Lr = round_up(L, kSmLabelTile);
         const int64_t most = (256LL << 20) / (2 * Bp) / kSmLabelTile * kSmLabelTile;
         keep = grad && sm_keep(B, Bp, Lr);
-        want = keep ? Lr : balanced(most < kSmLabelTile ? kSmLabelTile : most);
+        want = balanced(most < kSmLabelTile ? kSmLabelTile : most);
         const int64_t tiles = (Hp + kSmLabelTile - 1) / kSmLabelTile * (Bp / 128);
         size_t at = 0;
         auto take = [&](size_t n) {
@@ -129,7 +129,8 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.B = B; a.H = H; a.L = L; a.ldh = ldh; a.ldw = ldw; a.scale = scale;
     a.dW = dW; a.dh = dh; a.row_loss = row_loss; a.lse = lse; a.loss = loss;
     a.tn = l.tn; a.slices = sm_slices(B); a.narrow = sm_narrow(B, H, L); a.Bp = l.Bp; a.Hp = l.Hp;
-    a.Lc = l.want;
+    a.keep = l.keep && dtype == HASTE_BF16;
+    a.Lc = a.keep && workspace_bytes >= l.total(l.Lr, true) ? l.Lr : l.want;
     if (grad && workspace_bytes < l.total(l.want, true))
         a.Lc = l.balanced((int64_t)((workspace_bytes - l.dz) / l.block()) * kSmLabelTile);
     a.nv = (int32_t*)(w + l.nv);
@@ -138,7 +139,6 @@ int softmax_impl(bool grad, const void* h, const void* W, const int32_t* y_rowpt
     a.hit = (float*)(w + l.hit);
     a.clse = (float*)(w + l.clse);
     a.part = (float*)(w + l.part);
-    a.keep = l.keep && dtype == HASTE_BF16 && a.Lc == l.Lr;
     a.ref = (float*)(w + l.ref);
     a.redo = (int32_t*)(w + l.redo);
     a.own = (int32_t*)(w + l.own);
@@ -258,6 +258,13 @@ size_t haste_softmax_workspace_min(int64_t B, int64_t H, int64_t L, int grad)
 {
     if (check_softmax_shape(B, H, L) != HASTE_OK) return 0;
     return SoftmaxLayout(B, H, L, grad != 0).total(kSmLabelTile, grad != 0);
+}
+
+size_t haste_softmax_workspace_whole(int64_t B, int64_t H, int64_t L)
+{
+    if (check_softmax_shape(B, H, L) != HASTE_OK) return 0;
+    const SoftmaxLayout l(B, H, L, true);
+    return l.total(l.keep ? l.Lr : l.want, true);
 }
 
 int haste_softmax_loss(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,

@@ -6,16 +6,14 @@
 //   D = softmax(z) - [l in Y_b] / m_b,  dW = s D^T h,  dh = s D W.
 // A first pass forms the logits tile by tile and keeps one (maximum, sum) pair
 // per row and tile.  The gradients then need softmax(z) as an operand:
-//  - kept (a.keep: bf16, more than 128 rows, workspace for all labels): the
-//    first pass stores e = exp z itself, rounded to bf16, whose exponent range
-//    makes a common reference unnecessary.  softmax(z) = e / sum e, so the row's
-//    factor goes to the other operand: dW = (e)^T (h / sum e), and dh's rows
-//    are divided at their end.  Rows whose log-sum-exp lies outside 0 .. 64
-//    octaves are formed again as probabilities.  6 B L H operations and six
-//    bytes per logit.
-//  - else a second pass forms the logits again, piece of the label space by
-//    piece, as D in the workspace (two bytes per entry, Bp x Lc): eight
-//    B L H operations, and no more memory than one piece.
+//  - D goes to the workspace a piece of the label space at a time (two bytes per
+//    entry, Bp x Lc), formed from the logits again: eight B L H operations.
+//  - a.keep (bf16, more than 128 rows): the first pass leaves the first piece in
+//    place, as e = exp z itself: bf16's exponent range makes a reference
+//    unnecessary, and softmax(z) = e / sum e is left to the other operand, dW =
+//    e^T (h / sum e), and to the end of dh.  Rows whose log-sum-exp lies outside
+//    0 .. 64 octaves are formed again as probabilities.  Where one piece is all,
+//    six B L H operations do.
 //
 // Rows without labels are left out: the rows that have some are compacted
 // first (ranks), so padding costs no products and nothing in a padded row
@@ -28,11 +26,11 @@
 // entries of the labels themselves carry most of the gradient, and with
 // several labels per row they are p - 1 / m, often at the foot of a binade
 // where half a step is largest: what their rounding leaves (k_sm_labels) is
-// added to both gradients.  (With one label, -1 + p rounds well.)  Kept
-// exponentials hold them not at all.
+// added to both gradients.  (With one label, -1 + p rounds well.)  With a.keep
+// D goes without them, and they are added whole.
 //
 // Measured, whole step: 4096 x 131072 x 1024 bf16, a quarter of the rows
-// padding, 2.57 ms (963 TFLOP/s of 6 B L H; 3.33 ms with two passes); 128 x
+// padding, MS in four pieces and 2.57 in one (963 TFLOP/s of 6 B L H); 128 x
 // 89088 x 768 192 us; 1021 x 32003 x 640 fp16, 40 % padding, 192 us; 37 x 73 x
 // 96 32 us.
 #include "kernels.hpp"
@@ -395,7 +393,7 @@ __device__ __forceinline__ void row_results(const SoftmaxArgs& a, int64_t n, flo
 // two) per row.  kGradient: D = softmax of the piece of labels [l0, l0 + Lc),
 // without the labels' own terms.  kOneTile, for label spaces of one tile: the
 // rows' results and (grad) D at once, with no second pass and no k_sm_lse.
-// kKeep: as kStatistics, and the exponentials themselves stay in dz.
+// kKeep: as kStatistics, and the first piece's exponentials themselves stay in dz.
 enum Pass { kStatistics, kKeep, kGradient, kOneTile };
 template <int DT, int TN, Pass PASS>
 __device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, int64_t mt0, int64_t n0, int nv, bool grad,
@@ -476,6 +474,7 @@ __device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, in
             for (int nt = 0; nt < 2; ++nt) off[nt] = kDLog2<DT> - red[0][64 * wn + 32 * nt + r32][0];
         }
     }
+    if (PASS == kKeep && mt0 * kTM >= a.Lc) return;       // uniform: past the first piece
     if constexpr (PASS != kStatistics) {
         uint16_t* const dst = a.dz + dz_at(a, n0 + 64 * wn, mt0 * kTM + 128 * wm);
         store_tile<DT, TN>(
@@ -509,7 +508,7 @@ __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, in
     logits_tile<DT, TN, PASS>(a, l0, mt0, n0, nv, grad, ring, red);
 }
 
-// Forms the kept exponentials again, as probabilities, of rows whose logits lie
+// Forms the kept exponentials (the first piece's) again, as probabilities, of rows whose logits lie
 // too far from 0 (and of the other rows of their tiles, as they were).  Seldom
 // has work: 4 us without.
 template <int DT, int TN>
@@ -583,11 +582,11 @@ __device__ __forceinline__ int kept_each(int n) { return n > kSmList ? 0 : 2 * n
 // where all labels' two fit), so that it meets h itself in dW and is exact in
 // dh; in blocks that have too many, its place in dz takes it.
 template <int DT>
-__device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t i, int64_t l, float d, float up2)
+__device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t i, int64_t l0, int64_t l, float d,
+                                           float up2)
 {
-    const int64_t block = l / kTM;
-    const int n = a.own[block];
-    uint16_t* const at = a.dz + dz_at(a, i, l);
+    const int n = a.own[l / kTM];
+    uint16_t* const at = a.dz + dz_at(a, i, l - l0);
     float hi, none;
     if (n > kSmList || p >= a.rest_cap) {
         const uint32_t v = pack2<DT>(d * __builtin_amdgcn_exp2f(up2), 0.f);
@@ -600,7 +599,7 @@ __device__ __forceinline__ void keep_label(const SoftmaxArgs& a, int p, int64_t 
     a.rest[p] = d;
     unpack2<DT>(pack2<DT>(d, 0.f), hi, none);
     const int each = kept_each(n);
-    u32x4_t* const to = a.list + block * kSmList + a.slot[p] * each;
+    u32x4_t* const to = a.list + (l - l0) / kTM * kSmList + a.slot[p] * each;
     const uint32_t where = (uint32_t)i | (uint32_t)(l % kTM) << 20;
     to[0] = u32x4_t{2 * (uint32_t)p, where, __float_as_uint(hi), 0u};
     if (each == 2) to[1] = u32x4_t{2 * (uint32_t)p + 1, where, __float_as_uint(d - hi), 0u};
@@ -617,7 +616,7 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const float lse = live ? a.clse[i] : 0.f;
     const float up2 = a.keep && live ? lse - a.ref[i] : 0.f;     // dz is held times 2^up2
-    if (a.keep && blockIdx.y == 0) {
+    if (a.keep && l0 == 0 && blockIdx.y == 0) {
         const float f = __builtin_amdgcn_exp2f(-up2);
         for (int64_t j = 8 * threadIdx.x; j < a.Hp; j += 2048) {
             float x[8];
@@ -637,7 +636,7 @@ __global__ __launch_bounds__(256) void k_sm_labels(SoftmaxArgs a, int64_t l0)
         const float z = wave_dot<DT>(a, a.hc + i * a.Hp, l, lane);
         const float d = (__builtin_amdgcn_exp2f(fmaf(z, kLog2e, -lse)) - share) * kDScale<DT>;
         if (lane == 0 && a.keep) {
-            keep_label<DT>(a, p, i, l, d, up2);
+            keep_label<DT>(a, p, i, l0, l, d, up2);
         } else if (lane == 0) {
             const uint32_t hi = pack2<DT>(d, 0.f);
             a.dz[dz_at(a, i, l - l0)] = (uint16_t)hi;
@@ -777,7 +776,7 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
     if (s > 0) {
         rest = 0;
     } else if (nv > 0 && a.keep) {
-        const int own = a.own[n0 / kTM];
+        const int own = a.own[(l0 + n0) / kTM];
         rest = own * kept_each(own);
     } else if (nv > 0) {
         rest = a.count[n0 / kTM];
@@ -1169,7 +1168,7 @@ void run(bool grad, const SoftmaxArgs& a, hipStream_t s)
             const int64_t lt = (live + kTM - 1) / kTM;
             if (narrow) {
                 launch_narrow<DT, true>(a, l0, lt * kTM, span_of(lt * kTM), s);
-            } else if (!one && !a.keep) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
+            } else if (!one && !(a.keep && l0 == 0)) k_sm_logits<DT, TN, kGradient><<<(unsigned)(lt * nrt), NT, 0, s>>>(a, l0, true);
             k_sm_labels<DT><<<by_rank, 256, 0, s>>>(a, l0);
             const int64_t dw_tiles = (live + kGradTile - 1) / kGradTile * ncols * a.dw_splits;
             k_sm_grads<DT><<<(unsigned)(dh_grid + dw_tiles), 256, 0, s>>>(a, l0, ncols, l0 == 0, (uint32_t)dh_grid);

@@ -267,7 +267,7 @@ struct SoftmaxArgs {
     // workspace
     int64_t tn;             // rows per tile of the logits passes: sm_row_tile
     bool narrow;            // one row tile of 128 and a long label space: the streaming kernels
-    bool keep;              // the first pass leaves its exponentials in dz: sm_keep
+    bool keep;              // the first pass leaves the first piece's exponentials in dz: sm_keep
     int64_t Bp, Hp;         // B and H rounded up to tn and 64
     int64_t Lc;             // labels per piece, a multiple of kSmLabelTile
     int32_t* nv;
@@ -307,8 +307,7 @@ constexpr int64_t sm_row_tile(int64_t B, int64_t H, int64_t L)
 constexpr bool sm_narrow(int64_t B, int64_t H, int64_t L) { return B <= 128 && H <= 1024 && L >= 4096; }
 // Workgroups that count the labels by block, and blocks each can take.
 constexpr int64_t kSmBuckets = 64, kSmBucket = 2048;
-// Whether the exponentials of all labels are kept (given the workspace for
-// them, bf16 only): where the second pass costs more than the h that is written
+// Whether a bf16 step keeps the exponentials of its first piece (or all): where the second pass costs more than the h that is written
 // a second time and the look for rows to form again (us, kept against two
 // passes: 200 x 20000 x 768 92 and 103, 892 x 9527 x 904 160 and 195, 300 x
 // 12000 x 64 53.8 and 53.3).  Batches of up to 128 rows stream W in 35 us

@@ -535,7 +535,7 @@ int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq,
                      int64_t B, int64_t H, int64_t L, hipStream_t stream);
 
 /* Softmax cross entropy over a dense label matrix W (L x H), with its
- * gradient, without fp32 logits in memory.  Labels as CSR
+ * gradient, without the B x L logits being kept.  Labels as CSR
  * (y_rowptr, y_col); m_b = number of labels of row b:
  *   z = h W^T, lse_b = log sum_l exp z_bl,
  *   row_loss_b = lse_b - (1 / m_b) sum_{l in Y_b} z_bl,  loss = scale sum_b row_loss_b,
@@ -547,18 +547,20 @@ int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq,
  * summed in fp64.  D goes to the gradient products rounded to the operands'
  * type; what that leaves of the labels' own entries is added back, to dh for
  * up to 64 labels per row on average, to dW up to 512 per 256 label ids.
- * Where the workspace holds a bf16 step's whole D (large products of more than
- * 128 rows), it holds exp z and dW's h is rounded once more, times the row's
- * factor.  haste_softmax_loss computes loss, row_loss and lse alone.
+ * For more than 128 bf16 rows D is held as exp z, and h is rounded once more
+ * on its way to dW, times the row's factor.  haste_softmax_loss computes loss, row_loss and lse alone.
  * All results are bitwise repeatable for one workspace size.
  * H % 8 == 0, H <= 16384, ldh and ldw multiples of 8 up to 2^22, B <= 2^20,
  * L <= 2^31 - 65; pointers 16-byte aligned.
  * Workspace: any size from haste_softmax_workspace_min (256 labels at a
  * time) up; haste_softmax_workspace_size gives the size past which more does
- * not help (D whole, at two bytes per logit, up to 4 GiB for more than 128
- * rows, else in pieces of up to 256 MiB).  `grad`: for haste_softmax_step. */
+ * not help (pieces of up to 256 MiB of D), unless it is
+ * haste_softmax_workspace_whole: two bytes per logit for a bf16 step of more
+ * than 128 rows (up to 4 GiB; the same value elsewhere), which are then formed
+ * once instead of twice.  `grad`: for haste_softmax_step. */
 size_t haste_softmax_workspace_size(int64_t B, int64_t H, int64_t L, int grad);
 size_t haste_softmax_workspace_min(int64_t B, int64_t H, int64_t L, int grad);
+size_t haste_softmax_workspace_whole(int64_t B, int64_t H, int64_t L);
 int haste_softmax_loss(const void* h, const void* W, const int32_t* y_rowptr, const int32_t* y_col, float scale,
                        float* row_loss, float* lse, float* loss, int64_t B, int64_t H, int64_t L, int64_t ldh,
                        int64_t ldw, int dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
