@@ -30,9 +30,9 @@
 // D goes without them, and they are added whole.
 //
 // Measured, whole step: 4096 x 131072 x 1024 bf16, a quarter of the rows
-// padding, MS in four pieces and 2.57 in one (963 TFLOP/s of 6 B L H); 128 x
-// 89088 x 768 192 us; 1021 x 32003 x 640 fp16, 40 % padding, 192 us; 37 x 73 x
-// 96 32 us.
+// padding, 3.27 ms in four pieces and 2.53 in one (977 TFLOP/s of 6 B L H);
+// 128 x 89088 x 768 189 us; 1021 x 32003 x 640 fp16, 40 % padding, 187 us;
+// 37 x 73 x 96 32 us.
 #include "kernels.hpp"
 #include "tile.hpp"
 
@@ -490,7 +490,7 @@ __device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, in
 // Eight label tiles by the row tiles in turn.  Bound by the products and the
 // operands' way from L2 into LDS: 3072 live rows x 131072 x 1024 (statistics)
 // 800 us, 1030 TFLOP/s, of which the products alone are 607; with the
-// exponentials stored (kKeep) 930.  612 live rows x 32003 x 640 fp16 45 us.
+// exponentials stored (kKeep) 930 for all, 830 for a quarter.  612 live rows x 32003 x 640 fp16 45 us.
 template <int DT, int TN, Pass PASS>
 __global__ __launch_bounds__(kThreads<TN>, 2) void k_sm_logits(SoftmaxArgs a, int64_t l0, bool grad)
 {
