@@ -536,7 +536,8 @@ int haste_score_a8w8(const uint8_t* hq, const float* h_scale, const uint8_t* Wq,
 
 /* Softmax cross entropy over a dense label matrix W (L x H), with its
  * gradient, without the B x L logits being kept.  Labels as CSR
- * (y_rowptr, y_col); m_b = number of labels of row b:
+ * (y_rowptr, y_col, the ids of a row distinct); m_b = number of labels of
+ * row b:
  *   z = h W^T, lse_b = log sum_l exp z_bl,
  *   row_loss_b = lse_b - (1 / m_b) sum_{l in Y_b} z_bl,  loss = scale sum_b row_loss_b,
  *   D = softmax(z) - [l in Y_b] / m_b,  dW = scale D^T h,  dh = scale D W.
