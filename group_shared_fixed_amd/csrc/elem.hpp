@@ -57,31 +57,40 @@ constexpr int elem_bytes()
     return DT == HASTE_F32 ? 4 : 2;
 }
 
-// Eight consecutive elements as they lie in memory.
+// Eight consecutive elements as they lie in memory, of which the first `skip`
+// belong to the elements before.
 template <int DT>
 struct Raw8 {
     u32x4_t a[DT == HASTE_F32 ? 2 : 1];
+    int skip;
 };
 
-// Elements i .. i + 7 of p, of which n (1 <= n) exist; the rest read as 0.
+// Elements i .. i + 7 of p (whose first is 0), of which n (1 <= n) exist; the
+// rest widen to 0.  A row's last, partial eight are read as the eight that end
+// with it and shifted when they are widened, so that the loads of several
+// arrays stay in flight together; element by element, which only a first row
+// of less than eight takes, each would be a round trip to memory.  (Kernels pass
+// a constant 8 where rows are whole: what is left of this costs registers.)
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load8(const void* p, int64_t i, int64_t n)
 {
     Raw8<DT> r;
-    const char* q = reinterpret_cast<const char*>(p) + i * elem_bytes<DT>();
-    if (n >= 8) {
+    const int64_t over = n >= 8 ? 0 : 8 - n;
+    const char* q = reinterpret_cast<const char*>(p) + (i - over) * elem_bytes<DT>();
+    r.skip = (int)over;
+    if (over == 0 || i >= over) {
         r.a[0] = ldg16_any(q);
         if constexpr (DT == HASTE_F32) r.a[1] = ldg16_any(q + 16);
-    } else if constexpr (DT == HASTE_F32) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r.a[e / 4][e % 4] = e < n ? w[e] : 0u;
     } else {
-        const uint16_t* w = reinterpret_cast<const uint16_t*>(q);
+        uint32_t x[8] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = 2 * e < n ? w[2 * e] : 0u, hi = 2 * e + 1 < n ? w[2 * e + 1] : 0u;
-            r.a[0][e] = lo | (hi << 16);
+        for (int e = 0; e < 8; ++e)
+            if (e >= over) x[e] = DT == HASTE_F32 ? reinterpret_cast<const uint32_t*>(q)[e] : reinterpret_cast<const uint16_t*>(q)[e];
+        if constexpr (DT == HASTE_F32) {
+            r.a[0] = u32x4_t{x[0], x[1], x[2], x[3]};
+            r.a[1] = u32x4_t{x[4], x[5], x[6], x[7]};
+        } else {
+            r.a[0] = u32x4_t{x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16};
         }
     }
     return r;
@@ -96,6 +105,13 @@ __device__ __forceinline__ void widen8(const Raw8<DT>& r, float (&v)[8])
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) unpack2<DT>(r.a[0][e], v[2 * e], v[2 * e + 1]);
+    }
+    if (r.skip) {
+#pragma unroll
+        for (int b = 4; b >= 1; b /= 2)
+            if (r.skip & b)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = e + b < 8 ? v[e + b] : 0.f;
     }
 }
 

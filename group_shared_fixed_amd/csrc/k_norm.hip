@@ -12,9 +12,10 @@
 // added in a fixed order by a second kernel: bitwise repeatable).
 //
 // Both are bound by memory: every row is read once, into registers.  Measured:
-// forward 8192 x 4096 bf16 to codes 44 us (5.3 TB/s), 16411 x 768 bf16 with
-// residual, dropout, sum, y and rstd 20 us (5.1 TB/s), one row 2.9 us;
-// backward 16411 x 1024 bf16 34 us (4.9 TB/s) and 4.6 us for dgamma's sum.
+// forward 8192 x 4096 bf16 to codes 43 us (5.4 TB/s), 16411 x 768 bf16 with
+// residual, dropout, sum, y and rstd 19 us (5.3 TB/s), one row 2.9 us;
+// backward 16411 x 1024 bf16 34 us (4.9 TB/s) and 4.6 us for dgamma's sum,
+// 16411 x 1533, whose rows end inside a block of eight, 67 us.
 #include "elem.hpp"
 #include "kernels.hpp"
 
@@ -42,9 +43,14 @@ __device__ __forceinline__ float row_reduce(float v, float* sh)
     return v;
 }
 
+// Elements of a block of eight that exist: all of them unless rows are RAGGED
+// (cols % 8 != 0).
+template <bool RAGGED>
+__device__ __forceinline__ int64_t left(int64_t n) { return RAGGED ? n : 8; }
+
 // T threads per row, NV blocks of eight elements per thread, all loads of a
 // row in flight before the first is used.
-template <int DT, int T, int NV>
+template <int DT, int T, int NV, bool RAGGED>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop d)
 {
     constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -59,9 +65,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
     for (int k = 0; k < NV; ++k) {
         const int64_t b = t + (int64_t)k * T, c = 8 * b;
         if (b < per) {
-            rx[k] = load8<DT>(a.x, row * a.ldx + c, a.cols - c);
-            if (a.residual) rr[k] = load8<DT>(a.residual, row * a.ldr + c, a.cols - c);
-            rg[k] = load8<DT>(a.gamma, c, a.cols - c);
+            rx[k] = load8<DT>(a.x, row * a.ldx + c, left<RAGGED>(a.cols - c));
+            if (a.residual) rr[k] = load8<DT>(a.residual, row * a.ldr + c, left<RAGGED>(a.cols - c));
+            rg[k] = load8<DT>(a.gamma, c, left<RAGGED>(a.cols - c));
         }
     }
     const Philox g = drop_generator(d);
@@ -78,7 +84,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[k][e] += w[e];
             }
-            if (a.sum) store8<DT>(a.sum, row * a.cols + 8 * b, a.cols - 8 * b, v[k]);
+            if (a.sum) store8<DT>(a.sum, row * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), v[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss += v[k][e] * v[k][e];
         }
@@ -99,7 +105,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
                 v[k][e] = v[k][e] * rstd * w[e];
                 top = fmaxf(top, fabsf(v[k][e]));
             }
-            if (a.y) store8<DT>(a.y, row * a.cols + 8 * b, a.cols - 8 * b, v[k]);
+            if (a.y) store8<DT>(a.y, row * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), v[k]);
         }
     }
     if (a.q) {
@@ -110,14 +116,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm(NormArgs a, Drop
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t b = t + (int64_t)k * T;
-            if (b < per) store_e4m3(a.q, row * a.cols + 8 * b, a.cols - 8 * b, v[k], inv);
+            if (b < per) store_e4m3(a.q, row * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), v[k], inv);
         }
     }
 }
 
 // E4M3 rows with one scale of x as it is (the operand format of the scoring
 // call, for weights and for features that need no norm).
-template <int DT, int T, int NV>
+template <int DT, int T, int NV, bool RAGGED>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_quantize_rows(const void* x, int64_t ldx, int64_t rows,
                                                                      int64_t cols, uint8_t* q, float* scale)
 {
@@ -132,7 +138,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_quantize_rows(const void*
     for (int k = 0; k < NV; ++k) {
         const int64_t b = t + (int64_t)k * T;
         if (b < per) {
-            widen8<DT>(load8<DT>(x, row * ldx + 8 * b, cols - 8 * b), v[k]);
+            widen8<DT>(load8<DT>(x, row * ldx + 8 * b, left<RAGGED>(cols - 8 * b)), v[k]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[k][e]));
         }
@@ -144,14 +150,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_quantize_rows(const void*
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int64_t b = t + (int64_t)k * T;
-        if (b < per) store_e4m3(q, row * cols + 8 * b, cols - 8 * b, v[k], inv);
+        if (b < per) store_e4m3(q, row * cols + 8 * b, left<RAGGED>(cols - 8 * b), v[k], inv);
     }
 }
 
 // Workgroup w takes rows w RPB + r, w RPB + r + gridDim.x RPB, ...; its
 // partial of dgamma goes to part[w], kept in registers over its rows (one
 // partial per row would be as many bytes as dy).
-template <int DT, int T, int NV>
+template <int DT, int T, int NV, bool RAGGED>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs a, Drop d)
 {
     constexpr int RPB = T < 256 ? 256 / T : 1;
@@ -170,7 +176,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs 
         const int64_t b = t + (int64_t)k * T;
 #pragma unroll
         for (int e = 0; e < 8; ++e) gm[k][e] = dg[k][e] = 0.f;
-        if (b < per) widen8<DT>(load8<DT>(a.gamma, 8 * b, a.cols - 8 * b), gm[k]);
+        if (b < per) widen8<DT>(load8<DT>(a.gamma, 8 * b, left<RAGGED>(a.cols - 8 * b)), gm[k]);
     }
     for (int64_t row = (int64_t)blockIdx.x * RPB + r0; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         Raw8<DT> ry[NV], rs[NV], rd[NV];
@@ -178,9 +184,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs 
         for (int k = 0; k < NV; ++k) {
             const int64_t b = t + (int64_t)k * T, c = 8 * b;
             if (b < per) {
-                ry[k] = load8<DT>(a.dy, row * a.lddy + c, a.cols - c);
-                rs[k] = load8<DT>(a.sum, row * a.cols + c, a.cols - c);
-                if (a.dsum) rd[k] = load8<DT>(a.dsum, row * a.ldds + c, a.cols - c);
+                ry[k] = load8<DT>(a.dy, row * a.lddy + c, left<RAGGED>(a.cols - c));
+                rs[k] = load8<DT>(a.sum, row * a.cols + c, left<RAGGED>(a.cols - c));
+                if (a.dsum) rd[k] = load8<DT>(a.dsum, row * a.ldds + c, left<RAGGED>(a.cols - c));
             }
         }
         const float rstd = a.rstd[row];
@@ -216,10 +222,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs 
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ds[e] += w[e];
                 }
-                store8<DT>(a.dres, row * a.cols + 8 * b, a.cols - 8 * b, ds);
+                store8<DT>(a.dres, row * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), ds);
                 if (a.dx) {
                     if (d.thr) drop8(d, g, (uint64_t)(row * per + b), ds);
-                    store8<DT>(a.dx, row * a.cols + 8 * b, a.cols - 8 * b, ds);
+                    store8<DT>(a.dx, row * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), ds);
                 }
             }
         }
@@ -245,7 +251,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_norm_bwd(NormBwdArgs 
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int64_t b = t + (int64_t)k * T;
-        if (b < per) store8<HASTE_F32>(a.part, (int64_t)blockIdx.x * a.cols + 8 * b, a.cols - 8 * b, dg[k]);
+        if (b < per) store8<HASTE_F32>(a.part, (int64_t)blockIdx.x * a.cols + 8 * b, left<RAGGED>(a.cols - 8 * b), dg[k]);
     }
 }
 
@@ -273,7 +279,8 @@ __global__ __launch_bounds__(256) void k_column_sum(const float* part, int64_t n
 
 // Threads per row: a quarter or half of a wave up to 128 or 256 columns, one
 // wave up to 1024 (no barriers), 256 up to 8192, 1024 beyond.  (A whole wave
-// for 71 columns took 19 us instead of 8 for 22251 rows to codes.)
+// for 71 columns took 19 us instead of 8 for 22251 rows to codes; one wave for
+// 1536 79 instead of 63 in the backward pass of 16411.)
 template <typename F>
 void by_width(int64_t cols, F&& f)
 {
@@ -285,15 +292,20 @@ void by_width(int64_t cols, F&& f)
     else if (per <= 256) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
     else if (per <= 512) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
     else if (per <= 1024) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    else if (per <= 2048) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
     else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
 }
 
 template <typename F>
-void by_type(int dtype, F&& f)
+void by_type(int dtype, int64_t cols, F&& f)
 {
-    if (dtype == HASTE_BF16) f(std::integral_constant<int, HASTE_BF16>{});
-    else if (dtype == HASTE_F16) f(std::integral_constant<int, HASTE_F16>{});
-    else f(std::integral_constant<int, HASTE_F32>{});
+    auto ragged = [&](auto dt) {
+        if (cols % 8) f(dt, std::true_type{});
+        else f(dt, std::false_type{});
+    };
+    if (dtype == HASTE_BF16) ragged(std::integral_constant<int, HASTE_BF16>{});
+    else if (dtype == HASTE_F16) ragged(std::integral_constant<int, HASTE_F16>{});
+    else ragged(std::integral_constant<int, HASTE_F32>{});
 }
 
 unsigned row_groups(int64_t rows, int t) { return (unsigned)(t < 256 ? (rows * t + 255) / 256 : rows); }
@@ -302,10 +314,10 @@ unsigned row_groups(int64_t rows, int t) { return (unsigned)(t < 256 ? (rows * t
 
 void launch_add_norm(int dtype, const NormArgs& a, const Drop& d, hipStream_t s)
 {
-    by_type(dtype, [&](auto dt) {
+    by_type(dtype, a.cols, [&](auto dt, auto rg) {
         by_width(a.cols, [&](auto t, auto nv) {
             constexpr int T = decltype(t)::value;
-            k_add_norm<decltype(dt)::value, T, decltype(nv)::value>
+            k_add_norm<decltype(dt)::value, T, decltype(nv)::value, decltype(rg)::value>
                 <<<row_groups(a.rows, T), T < 256 ? 256 : T, 0, s>>>(a, d);
         });
     });
@@ -314,36 +326,42 @@ void launch_add_norm(int dtype, const NormArgs& a, const Drop& d, hipStream_t s)
 void launch_quantize_rows(int dtype, const void* x, int64_t ldx, int64_t rows, int64_t cols, uint8_t* q, float* scale,
                           hipStream_t s)
 {
-    by_type(dtype, [&](auto dt) {
+    by_type(dtype, cols, [&](auto dt, auto rg) {
         by_width(cols, [&](auto t, auto nv) {
             constexpr int T = decltype(t)::value;
-            k_quantize_rows<decltype(dt)::value, T, decltype(nv)::value>
+            k_quantize_rows<decltype(dt)::value, T, decltype(nv)::value, decltype(rg)::value>
                 <<<row_groups(rows, T), T < 256 ? 256 : T, 0, s>>>(x, ldx, rows, cols, q, scale);
         });
     });
 }
 
 // Enough workgroups to keep every CU's memory queues full, few enough that
-// the dgamma partials stay small next to the rows themselves (2128 x 5048:
-// 512 groups 31 us, 1024 39 us).
+// the dgamma partials stay small next to the rows themselves (us with 512 and
+// 1024: 2128 x 5048 31 and 39, 8192 x 4096 67 and 73, 9000 x 2040 42 and 45,
+// 16411 x 1536 59 and 54).  A few rows take one group and no second kernel (16 x
+// 768 10.2 us a call, 12.4 with it).
 int64_t norm_bwd_groups(int64_t rows, int64_t cols)
 {
-    const int64_t per = cols <= 128 ? 16 : cols <= 256 ? 8 : cols <= 1024 ? 4 : 1;      // rows per workgroup
-    const int64_t want = (rows + per - 1) / per, most = cols <= 1024 ? 1024 : 512;
+    const int64_t per = cols <= 128 ? 16 : cols <= 256 ? 8 : cols <= 1024 ? 4 : 1;  // rows per workgroup
+    if (cols <= 1024 && rows <= 4 * per) return 1;
+    const int64_t want = (rows + per - 1) / per, most = cols <= 1024 || (cols <= 1536 && rows >= 8192) ? 1024 : 512;
     return want < most ? want : most;
 }
 
 void launch_add_norm_bwd(int dtype, const NormBwdArgs& a, const Drop& d, hipStream_t s)
 {
     const int64_t n = norm_bwd_groups(a.rows, a.cols);
-    by_type(dtype, [&](auto dt) {
-        by_width(a.cols, [&](auto t, auto nv) {
+    NormBwdArgs b = a;
+    if (n == 1 && a.part) b.part = a.dgamma;
+    by_type(dtype, a.cols, [&](auto dt, auto rg) {
+        auto launch = [&](auto t, auto nv) {
             constexpr int T = decltype(t)::value;
-            k_add_norm_bwd<decltype(dt)::value, T, decltype(nv)::value>
-                <<<(unsigned)n, T < 256 ? 256 : T, 0, s>>>(a, d);
-        });
+            k_add_norm_bwd<decltype(dt)::value, T, decltype(nv)::value, decltype(rg)::value>
+                <<<(unsigned)n, T < 256 ? 256 : T, 0, s>>>(b, d);
+        };
+        by_width(a.cols, launch);
     });
-    if (a.part) k_column_sum<<<(unsigned)((a.cols + 15) / 16), 256, 0, s>>>(a.part, n, a.cols, a.dgamma);
+    if (a.part && n > 1) k_column_sum<<<(unsigned)((a.cols + 15) / 16), 256, 0, s>>>(a.part, n, a.cols, a.dgamma);
 }
 
 }  // namespace haste

@@ -31,7 +31,7 @@
 //
 // Measured, whole step: 4096 x 131072 x 1024 bf16, a quarter of the rows
 // padding, 3.27 ms in four pieces and 2.53 in one (977 TFLOP/s of 6 B L H);
-// 128 x 89088 x 768 189 us; 1021 x 32003 x 640 fp16, 40 % padding, 187 us;
+// 128 x 89088 x 768 192 us; 1021 x 32003 x 640 fp16, 40 % padding, 190 us;
 // 37 x 73 x 96 32 us.
 #include "kernels.hpp"
 #include "tile.hpp"

@@ -19,7 +19,7 @@ SEED, OFFSET = 0x0123456789ABCDEF, (1 << 63) + 12345
 # odd widths, one element, one row, widths around the eight-element blocks and
 # around each thread-count rule (512, 1024, 2048, 4096, 8192 columns)
 SHAPES = [(1, 1), (1, 768), (3, 7), (37, 96), (5, 513), (9, 1001), (4, 1025), (130, 2050), (3, 4099), (2, 8192),
-          (2, 8200), (2, 32768), (1023, 40)]
+          (2, 8200), (2, 32768), (1023, 40), (64, 1003), (2100, 129), (3, 12_001)]
 
 
 def _x(rng, rows, cols, t):
