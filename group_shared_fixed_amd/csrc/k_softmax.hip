@@ -488,7 +488,7 @@ __device__ __forceinline__ void logits_tile(const SoftmaxArgs& a, int64_t l0, in
 }
 
 // Eight label tiles by the row tiles in turn.  Bound by the products and the
-// operands' way from L2 into LDS: 3072 live rows x 131072 x 1024 (statistics)
+// operands' way from L2 into LDS: 3/4 of 4096 rows x 131072 x 1024 (statistics)
 // 800 us, 1030 TFLOP/s, of which the products alone are 607; with the
 // exponentials stored (kKeep) 930 for all, 830 for a quarter.  612 live rows x 32003 x 640 fp16 45 us.
 template <int DT, int TN, Pass PASS>
@@ -804,7 +804,7 @@ __device__ __forceinline__ void dw_tile(const SoftmaxArgs& a, int64_t l0, int64_
 
 // The gradients take the narrow tile at every batch: two workgroups per CU
 // fill the chip more evenly with the few tiles and long contractions they have.
-// 3072 live rows x 131072 x 1024 1.58 ms (1044 TFLOP/s); 128 x 89088 x 768
+// 3/4 of 4096 rows x 131072 x 1024 1.58 ms (1044 TFLOP/s); 128 x 89088 x 768
 // 92 us: four stages per tile of dW, whose latency with its list and its
 // 137 MB of stores is half of it.
 constexpr int kGradTile = 128;

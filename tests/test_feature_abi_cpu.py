@@ -115,6 +115,12 @@ def test_softmax_workspace_is_bounded(L):
     # the gradient matrix of 4096 x 131072 would be 1 GiB; a piece of it is at most 256 MiB
     full, least = (f(4096, 1024, 131072, 1) for f in (L.haste_softmax_workspace_size, L.haste_softmax_workspace_min))
     assert full - least <= 256 << 20
+    # asked for, the whole of it: two bytes per logit more than the least, for a step that can keep it
+    whole = L.haste_softmax_workspace_whole(4096, 1024, 131072)
+    assert 1 << 30 <= whole - least + (2 << 20) <= (1 << 30) + (16 << 20)
+    assert L.haste_softmax_workspace_whole(128, 1024, 131072) == L.haste_softmax_workspace_size(128, 1024, 131072, 1)
+    assert L.haste_softmax_workspace_whole(4096, 1023, 131072) == 0
+    assert hs.softmax_workspace_size(4096, 1024, 131072, whole=True) == whole
 
 
 def test_binding_refuses():
