@@ -203,6 +203,8 @@ __global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
                 float* const z = a.Z + b * a.L + l;
                 if (vec && l + 4 <= a.L) {
                     stg_stream(z, v);
+                } else if (l + 4 <= a.L) {
+                    stg16_any(z, __builtin_bit_cast(u32x4_t, v));
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
