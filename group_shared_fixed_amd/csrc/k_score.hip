@@ -177,7 +177,9 @@ __global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
         const int64_t l = l0 + 64 * w + 32 * nt + r32;
         sw[nt] = l < a.L ? a.ws[l] : 0.f;
     }
-    const bool vec = (a.L & 3) == 0;
+    // more than the caches hold goes past them, if in whole lines (us past and
+    // through them: 2048 x 89088 x 768 314 and 370, 573 x 29240 x 240 33 and 30)
+    const bool stream = (a.L & 3) == 0 && a.B * a.L > (256LL << 20) / 4;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(256, 2) void k_score_tiles(ScoreArgs a)
                 if (b >= a.B) continue;
                 v *= a.hs[b];
                 float* const z = a.Z + b * a.L + l;
-                if (vec && l + 4 <= a.L) {
+                if (stream && l + 4 <= a.L) {
                     stg_stream(z, v);
                 } else if (l + 4 <= a.L) {
                     stg16_any(z, __builtin_bit_cast(u32x4_t, v));
