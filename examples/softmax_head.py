@@ -14,7 +14,7 @@ The encoder is replaced by synthetic outputs: noise plus the sum of a fixed
 direction per positive label, so that there is something to learn.
 
     python3 examples/softmax_head.py                         # the small head-tail workload's head
-    python3 examples/softmax_head.py --labels 89088 --width 768 --batch 128 --steps 20
+    python3 examples/softmax_head.py --labels 89088 --width 768 --batch 128 --lr 0.5   # that size; 60 steps learn little
 """
 
 import argparse
